@@ -25,7 +25,7 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 CK_OK, CK_ERR_INVALID_ARG, CK_ERR_UNSUPPORTED, CK_ERR_CUDA, CK_ERR_TIMEOUT = range(5)
-CK_BF16, CK_FP16 = 0, 1
+CK_BF16, CK_FP16, CK_FP32 = 0, 1, 2
 STATUS_NAMES = {0: "CK_OK", 1: "CK_ERR_INVALID_ARG", 2: "CK_ERR_UNSUPPORTED", 3: "CK_ERR_CUDA",
                 4: "CK_ERR_TIMEOUT"}
 
@@ -59,6 +59,15 @@ SIGNATURES = {
     "ck_gemv_w4a8": [_p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p],
     "ck_gemv_w4a8_tc": [_p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p],
     "ck_gemv_awq_w4a16": [_p, _int, _i64, _i64, _i64, _int, _p, _p, _p, _p, _p, _p],
+    "ck_moe_route": [_p, _int, _i64, _i64, _int, _int, _p, _p, _p],
+    "ck_moe_awq_w4a16_workspace_bytes": [_i64, _int, _i64],
+    "ck_moe_awq_w4a16": [_p, _int, _i64, _i64, _i64, _i64, _i64, _int, _p, _int, _int, _int, _p, _p, _p, _p, _p, _p,
+                         _p, _p, ctypes.c_size_t, _p],
+    "ck_moe_experts_awq_w4a16": [_p, _int, _i64, _i64, _i64, _i64, _i64, _int, _p, _p, _int, _p, _p, _p, _p, _p, _p,
+                                 _p, _p, ctypes.c_size_t, _p],
+    "ck_lora_add_workspace_bytes": [_i64, _i64],
+    "ck_lora_add": [_p, _int, _p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p,
+                    ctypes.c_size_t, _p],
     "ck_gemm_w4a4_i32": [_p, _p, _i64, _i64, _i64, _p, _p],
     "ck_gemm_w4a8_i32": [_p, _p, _i64, _i64, _i64, _p, _p],
     "ck_device_error_check": [_p],
@@ -67,6 +76,7 @@ SIGNATURES = {
     "ck_version": [],
 }
 _RESTYPES = {"ck_linear_w4a4_workspace_bytes": ctypes.c_size_t, "ck_linear_w4a8_workspace_bytes": ctypes.c_size_t,
+             "ck_moe_awq_w4a16_workspace_bytes": ctypes.c_size_t, "ck_lora_add_workspace_bytes": ctypes.c_size_t,
              "ck_last_error": ctypes.c_char_p, "ck_version": ctypes.c_char_p}
 
 for _name, _args in SIGNATURES.items():
@@ -166,6 +176,9 @@ def last_error() -> str:
 
 def _call(dev, name: str, *args, stream=None) -> None:
     """Calls the C entry point `name` with `dev` current and that device's stream appended."""
+    if stream is None and torch.cuda.current_device() == dev.index:     # the common case, without a device guard
+        _check(getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
+        return
     with torch.cuda.device(dev):
         _check(getattr(lib, name)(*args, _stream(stream, dev)), name)
 
@@ -432,6 +445,163 @@ def gemv_awq_w4a16(x, qweight, wscales, wzeros, bias=None, group_size: int = 64,
     out = _mn_out(x, M, N, out, x.dtype)
     _call(_cuda(x, out), "ck_gemv_awq_w4a16", _ptr(x), _dtype_code(x.dtype), M, K, N, group_size, _ptr(qweight),
           _ptr(wscales), _ptr(wzeros), _ptr(bias), _ptr(out), stream=stream)
+    return out
+
+
+# ------------------------------------------ weights chosen for each token
+
+_LOGITS = (torch.bfloat16, torch.float16, torch.float32)
+
+
+def _empty(shape, dtype, dev, stream):
+    """A tensor for the call's own use or its result, from the pool of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _shape(where: str, **named) -> None:
+    """ValueError unless each named tensor (None is skipped) is contiguous and has its shape."""
+    for name, (t, shape) in named.items():
+        if t is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{where}: {name} must be a contiguous tensor of shape {shape}, got {tuple(t.shape)}"
+                             f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+
+
+def _matrix(where: str, name: str, t, cols=None) -> None:
+    """ValueError unless t is 2-D with a contiguous last dimension (of `cols` entries)."""
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{where}: {name} must be a 2-D tensor with contiguous rows"
+                         f"{'' if cols is None else f' of {cols} entries'}, got {tuple(t.shape)}")
+
+
+def _ld(t) -> int:
+    """Row stride of a 2-D tensor; that of a single row is its length whatever the tensor says."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def moe_route(logits, top_k: int, renormalize: bool = True, weights_out=None, ids_out=None, stream=None):
+    """The top_k largest of each row of logits (T, E): (weights (T, top_k) float32, ids (T, top_k) int32).
+
+    weights are softmax shares among the chosen (renormalize) or among all E experts; ties go to the
+    lowest index; a -inf or NaN logit is never chosen, and a slot left over has id -1 and weight 0."""
+    _types("moe_route", logits=(logits, _LOGITS), weights_out=(weights_out, _F32), ids_out=(ids_out, _I32))
+    if logits.dim() != 2:
+        raise ValueError(f"moe_route: logits must be (T, E), got {tuple(logits.shape)}")
+    T, E = logits.shape
+    _shape("moe_route", logits=(logits, (T, E)), weights_out=(weights_out, (T, top_k)), ids_out=(ids_out, (T, top_k)))
+    dev = _cuda(logits, weights_out, ids_out)
+    k = max(int(top_k), 0)
+    weights = _empty((T, k), torch.float32, dev, stream) if weights_out is None else weights_out
+    ids = _empty((T, k), torch.int32, dev, stream) if ids_out is None else ids_out
+    _call(dev, "ck_moe_route", logits.data_ptr(), _LOGITS.index(logits.dtype), T, E, int(top_k), int(bool(renormalize)),
+          weights.data_ptr(), ids.data_ptr(), stream=stream)
+    return weights, ids
+
+
+def moe_awq_w4a16_workspace_bytes(T: int, top_k: int, I: int) -> int:
+    return int(lib.ck_moe_awq_w4a16_workspace_bytes(T, top_k, I))
+
+
+def _moe(name, x, given, choice, top_k, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, group_size, workspace, out,
+         stream):
+    """Shared marshalling of the mixture-of-experts calls; `given` are the tensors of the choice, `choice`
+    the C arguments between the group size and the weights."""
+    same = (x.dtype,) if x.dtype in _HALF else _HALF
+    _types(name, x=(x, _HALF), gate_up_q=(gate_up_q, _BYTES), gate_up_s=(gate_up_s, same), gate_up_z=(gate_up_z, same),
+           down_q=(down_q, _BYTES), down_s=(down_s, same), down_z=(down_z, same), out=(out, same),
+           workspace=(workspace, _BYTES))
+    _matrix(name, "x", x)
+    T, K = x.shape
+    if gate_up_q.dim() != 3 or gate_up_q.shape[1] % 2:
+        raise ValueError(f"{name}: gate_up_q must be (E, 2 I, K / 2), got {tuple(gate_up_q.shape)}")
+    E, I = gate_up_q.shape[0], gate_up_q.shape[1] // 2
+    G = int(group_size)
+    if G > 0:
+        _shape(name, gate_up_q=(gate_up_q, (E, 2 * I, K // 2)), gate_up_s=(gate_up_s, (E, K // G, 2 * I)),
+               gate_up_z=(gate_up_z, (E, K // G, 2 * I)), down_q=(down_q, (E, K, I // 2)),
+               down_s=(down_s, (E, I // G, K)), down_z=(down_z, (E, I // G, K)), out=(out, (T, K)))
+    dev = _cuda(x, *given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, workspace, out)
+    if workspace is None:
+        workspace = _empty((moe_awq_w4a16_workspace_bytes(T, top_k, I),), torch.uint8, dev, stream)
+    if out is None:
+        out = _empty((T, K), x.dtype, dev, stream)
+    _call(dev, "ck_" + name, x.data_ptr(), _dtype_code(x.dtype), T, K, I, E, _ld(x), G, *choice, gate_up_q.data_ptr(),
+          gate_up_s.data_ptr(), gate_up_z.data_ptr(), down_q.data_ptr(), down_s.data_ptr(), down_z.data_ptr(),
+          out.data_ptr(), workspace.data_ptr(), _nbytes(workspace), stream=stream)
+    return out
+
+
+def moe_awq_w4a16(x, logits, top_k: int, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z,
+                  group_size: int = 64, renormalize: bool = True, workspace=None, out=None, stream=None):
+    """A mixture-of-experts layer for up to 64 tokens: each row of x (T, K) goes through the top_k experts of
+    its logits (T, E) as moe_route chooses them, out = sum of weight * (silu(x Wgate^T) * (x Wup^T)) Wdown^T.
+
+    The experts are AWQ W4A16: gate_up_q (E, 2 I, K/2) packed bytes, the gate rows first, with scales and
+    zeros (E, K/G, 2 I); down_q (E, K, I/2) with scales and zeros (E, I/G, K), all in x's dtype."""
+    name = "moe_awq_w4a16"
+    _types(name, logits=(logits, _LOGITS))
+    _shape(name, logits=(logits, (x.shape[0], gate_up_q.shape[0])))
+    choice = (logits.data_ptr(), _LOGITS.index(logits.dtype), int(top_k), int(bool(renormalize)))
+    return _moe(name, x, (logits,), choice, int(top_k), gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z,
+                group_size, workspace, out, stream)
+
+
+def moe_experts_awq_w4a16(x, ids, weights, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z,
+                          group_size: int = 64, workspace=None, out=None, stream=None):
+    """moe_awq_w4a16 with the choice given: ids (T, top_k) int32 and weights (T, top_k) float32, used as they
+    are. A slot whose id is outside [0, E) is empty; an expert named twice counts with both weights."""
+    name = "moe_experts_awq_w4a16"
+    _types(name, ids=(ids, _I32), weights=(weights, _F32))
+    if ids.dim() != 2:
+        raise ValueError(f"{name}: ids must be (T, top_k), got {tuple(ids.shape)}")
+    k = ids.shape[1]
+    _shape(name, ids=(ids, (x.shape[0], k)), weights=(weights, (x.shape[0], k)))
+    return _moe(name, x, (ids, weights), (ids.data_ptr(), weights.data_ptr(), k), k, gate_up_q, gate_up_s, gate_up_z,
+                down_q, down_s, down_z, group_size, workspace, out, stream)
+
+
+def lora_add_workspace_bytes(M: int, L: int) -> int:
+    return int(lib.ck_lora_add_workspace_bytes(M, L))
+
+
+def lora_add(y, x, lora_a, lora_b, ids, scales=None, workspace=None, out=None, stream=None):
+    """out[m] = y[m] + scales[a] * (x[m] A[a]^T) B[a]^T with a = ids[m]; out[m] = y[m] where a is no adapter.
+
+    y (M, N) bf16 or x's dtype is a projection's output, x (M, K) its input; lora_a (L, R, K) and lora_b
+    (L, N, R) are the adapters, ids (M,) int32 (-1: none), scales (L,) float32. `out` may be y: in place."""
+    same = (x.dtype,) if x.dtype in _HALF else _HALF
+    half = same + _BF16
+    _types("lora_add", y=(y, half), x=(x, _HALF), lora_a=(lora_a, same), lora_b=(lora_b, same), ids=(ids, _I32),
+           scales=(scales, _F32), out=(out, (y.dtype,)), workspace=(workspace, _BYTES))
+    _matrix("lora_add", "x", x)
+    M, K = x.shape
+    if lora_a.dim() != 3 or lora_b.dim() != 3:
+        raise ValueError("lora_add: lora_a must be (L, R, K) and lora_b (L, N, R)")
+    L, R = lora_a.shape[:2]
+    N = lora_b.shape[1]
+    _matrix("lora_add", "y", y, N)
+    if y.shape[0] != M:
+        raise ValueError(f"lora_add: y has {y.shape[0]} rows, x {M}")
+    _shape("lora_add", lora_a=(lora_a, (L, R, K)), lora_b=(lora_b, (L, N, R)), ids=(ids, (M,)), scales=(scales, (L,)))
+    dev = _cuda(y, x, lora_a, lora_b, ids, scales, workspace, out)
+    if out is None:
+        out = _empty((M, N), y.dtype, dev, stream)
+    else:
+        _matrix("lora_add", "out", out, N)
+        if out.shape[0] != M:
+            raise ValueError(f"lora_add: out has {out.shape[0]} rows, x {M}")
+    if workspace is None:
+        need = lora_add_workspace_bytes(M, L)
+        ws_ptr, ws_bytes = None, 0
+        if need:
+            workspace = _empty((need,), torch.uint8, dev, stream)
+    if workspace is not None:
+        ws_ptr, ws_bytes = workspace.data_ptr(), _nbytes(workspace)
+    _call(dev, "ck_lora_add", y.data_ptr(), _dtype_code(y.dtype), x.data_ptr(), _dtype_code(x.dtype), M, K, N, R, L,
+          _ld(x), _ld(y), _ld(out), lora_a.data_ptr(), lora_b.data_ptr(), ids.data_ptr(),
+          None if scales is None else scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes, stream=stream)
     return out
 
 

@@ -23,6 +23,8 @@
 #include "gemv_w4a8.cuh"
 #include "gemv_w4a8_stream.cuh"
 #include "gemv_w4a8_tc.cuh"
+#include "lora_add.cuh"
+#include "moe_awq.cuh"
 #include "rotate_quant.cuh"
 #include "rotate_quant_general.cuh"
 
@@ -1332,3 +1334,5 @@ extern "C" ck_status ck_selftest_bounded_wait(int64_t timeout_ns, void* stream) 
   selftest_wait_kernel<<<1, 32, 0, S(stream)>>>((uint64_t)timeout_ns);
   return launch_status("selftest_bounded_wait");
 }
+
+#include "ck_api_chosen.cuh"

@@ -1,0 +1,307 @@
+// Host side of the operators whose weights are chosen for each token: expert
+// routing, the mixture-of-experts layer and the low-rank adapters. Included by
+// ck_api.cu, whose helpers (fail, launch_status, aligned, S, sm_count) it uses.
+
+namespace {
+
+// Launches `kern` as a programmatic dependent (see launch_pdl) with clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, unsigned cluster, unsigned block, size_t smem,
+                           cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+bool known_float(ck_dtype t) { return t == CK_BF16 || t == CK_FP16; }
+
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// ------------------------------------------------------------------ routing
+
+ck_status check_choice(const char* who, int64_t E, int top_k) {
+  using namespace ck::moe;
+  if (E <= 0 || top_k <= 0) return fail(CK_ERR_INVALID_ARG, "%s: E and top_k must be > 0", who);
+  if (E > kMaxExperts) return fail(CK_ERR_UNSUPPORTED, "%s: E=%lld > %d", who, (long long)E, kMaxExperts);
+  if (top_k > kMaxTopK) return fail(CK_ERR_UNSUPPORTED, "%s: top_k=%d > %d", who, top_k, kMaxTopK);
+  if (top_k > E) return fail(CK_ERR_INVALID_ARG, "%s: top_k=%d > E=%lld", who, top_k, (long long)E);
+  return CK_OK;
+}
+
+ck_status check_logits(const char* who, const void* logits, ck_dtype lt) {
+  if (!known_float(lt) && lt != CK_FP32) return fail(CK_ERR_INVALID_ARG, "%s: unknown logits dtype", who);
+  if (!logits) return fail(CK_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(logits, lt == CK_FP32 ? 4 : 2)) return fail(CK_ERR_INVALID_ARG, "%s: misaligned logits", who);
+  return CK_OK;
+}
+
+// -------------------------------------------------------- mixture of experts
+
+template <typename T, int NT>
+cudaError_t launch_gate_up(const ck::moe::Params& p, cudaStream_t st) {
+  using namespace ck::moe;
+  auto kern = gate_up_kernel<T, NT>;
+  struct Tag {};
+  const cudaError_t e = set_smem_max<Tag>(kern, (int)sizeof(GateUpSmem<NT>));
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)p.choice.T * p.choice.k * (p.I / kColsItem);   // a unit has a slot at least
+  const unsigned grid = (unsigned)std::min<int64_t>(most, 2 * sm_count());
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), sizeof(GateUpSmem<NT>), st, p);
+}
+
+template <typename T, int NT>
+cudaError_t launch_down(const ck::moe::Params& p, cudaStream_t st) {
+  using namespace ck::moe;
+  auto kern = down_kernel<T, NT>;
+  struct Tag {};
+  const size_t smem = sizeof(DownSmem) + (size_t)kWarps * p.choice.T * kRowsTile * 4;
+  const cudaError_t e = set_smem_max<Tag>(kern, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int tiles = p.K / kRowsTile;
+  int cs = 8;
+  while (cs > 1 && tiles * cs > 2 * sm_count()) cs /= 2;
+  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kThreads, smem, st, p);
+}
+
+template <typename T>
+cudaError_t launch_moe(const ck::moe::Params& p, cudaStream_t st) {
+  cudaError_t e;
+  if (p.choice.T <= 8) e = launch_gate_up<T, 1>(p, st);
+  else if (p.choice.T <= 16) e = launch_gate_up<T, 2>(p, st);
+  else e = launch_gate_up<T, 4>(p, st);
+  if (e != cudaSuccess) return e;
+  if (p.choice.T <= 4) return launch_down<T, 1>(p, st);
+  if (p.choice.T <= 8) return launch_down<T, 2>(p, st);
+  return launch_down<T, 4>(p, st);
+}
+
+struct MoeArgs {
+  const void* x;
+  ck_dtype dt;
+  int64_t T, K, I, E, ldx;
+  int G;
+  const uint8_t* gq;
+  const void *gs, *gz;
+  const uint8_t* dq;
+  const void *ds, *dz;
+  void *out, *ws;
+  size_t ws_bytes;
+};
+
+ck_status moe_impl(const char* who, const MoeArgs& a, const ck::moe::Choice& choice, cudaStream_t st) {
+  using namespace ck::moe;
+  if (a.T < 0 || a.K <= 0 || a.I <= 0) return fail(CK_ERR_INVALID_ARG, "%s: T must be >= 0, K and I > 0", who);
+  if (!known_float(a.dt)) return fail(CK_ERR_INVALID_ARG, "%s: unknown dtype", who);
+  if (a.T > kMaxTokens) return fail(CK_ERR_UNSUPPORTED, "%s: T=%lld > %d", who, (long long)a.T, kMaxTokens);
+  if (a.G != 64 && a.G != 128 && a.G != 256)
+    return fail(CK_ERR_UNSUPPORTED, "%s: group_size=%d must be 64, 128 or 256", who, a.G);
+  if (a.K % a.G != 0 || a.I % a.G != 0)
+    return fail(CK_ERR_INVALID_ARG, "%s: K and I must be multiples of group_size", who);
+  if (a.K > (1 << 20) || a.I > (1 << 20)) return fail(CK_ERR_UNSUPPORTED, "%s: dimension too large", who);
+  if (a.T == 0) return ok();
+  if (a.ldx < a.K || a.ldx % 8 != 0)
+    return fail(CK_ERR_INVALID_ARG, "%s: ldx=%lld must be >= K and a multiple of 8", who, (long long)a.ldx);
+  if (!a.x || !a.gq || !a.gs || !a.gz || !a.dq || !a.ds || !a.dz || !a.out || !a.ws)
+    return fail(CK_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(a.x, 16) || !aligned(a.gq, 16) || !aligned(a.dq, 16) || !aligned(a.gs, 16) || !aligned(a.gz, 16) ||
+      !aligned(a.ds, 16) || !aligned(a.dz, 16))
+    return fail(CK_ERR_INVALID_ARG, "%s: x, the weights, scales and zeros must be 16-byte aligned", who);
+  if (!aligned(a.out, 2)) return fail(CK_ERR_INVALID_ARG, "%s: misaligned output", who);
+  if (!aligned(a.ws, 256)) return fail(CK_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+  const size_t need = ck_moe_awq_w4a16_workspace_bytes(a.T, choice.k, a.I);
+  if (a.ws_bytes < need)
+    return fail(CK_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", who, a.ws_bytes, need);
+  Params p;
+  p.choice = choice;
+  p.x = a.x; p.ldx = a.ldx; p.K = (int)a.K; p.I = (int)a.I;
+  p.gsh = a.G == 64 ? 0 : a.G == 128 ? 1 : 2;
+  p.gate_up_q = a.gq; p.gate_up_s = a.gs; p.gate_up_z = a.gz;
+  p.down_q = a.dq; p.down_s = a.ds; p.down_z = a.dz;
+  p.h = reinterpret_cast<__nv_bfloat16*>(a.ws);
+  p.out = a.out;
+  const cudaError_t e = a.dt == CK_BF16 ? launch_moe<__nv_bfloat16>(p, st) : launch_moe<__half>(p, st);
+  if (e != cudaSuccess) return fail(CK_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  return launch_status(who);
+}
+
+// ----------------------------------------------------------------- adapters
+
+template <typename T, typename TY, int RC, int TM>
+cudaError_t launch_lora_tm(const ck::lora::Params& p, int64_t tiles, cudaStream_t st) {
+  using namespace ck::lora;
+  auto kern = lora_kernel<T, TY, RC, TM>;
+  using SM = Smem<RC, TM>;
+  struct Tag {};
+  const cudaError_t e = set_smem_max<Tag>(kern, (int)sizeof(SM), (int)sizeof(SM));
+  if (e != cudaSuccess) return e;
+  int cs = 8;
+  while (cs > 1 && tiles * cs > 2 * sm_count() && TM > 16) cs /= 2;
+  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kThreads, sizeof(SM), st, p);
+}
+
+template <typename T, typename TY>
+cudaError_t launch_lora(const ck::lora::Params& p, int tm, int64_t tiles, cudaStream_t st) {
+  if (tm == 16) {
+    if (p.R <= 32) return launch_lora_tm<T, TY, 1, 16>(p, tiles, st);
+    if (p.R <= 64) return launch_lora_tm<T, TY, 2, 16>(p, tiles, st);
+    return launch_lora_tm<T, TY, 4, 16>(p, tiles, st);
+  }
+  if (p.R <= 32) return launch_lora_tm<T, TY, 1, 64>(p, tiles, st);
+  if (p.R <= 64) return launch_lora_tm<T, TY, 2, 64>(p, tiles, st);
+  return launch_lora_tm<T, TY, 4, 64>(p, tiles, st);
+}
+
+// Tokens of a tile, by how many tokens an adapter has on average.
+int lora_tile(int64_t M, int64_t L) { return M >= 512 && M >= 16 * L ? 64 : 16; }
+
+}  // namespace
+
+extern "C" {
+
+ck_status ck_moe_route(const void* logits, ck_dtype lt, int64_t T, int64_t E, int top_k, int renormalize,
+                       float* weights, int32_t* ids, void* stream) {
+  const char* who = "moe_route";
+  if (T < 0) return fail(CK_ERR_INVALID_ARG, "%s: T must be >= 0", who);
+  ck_status r = check_choice(who, E, top_k);
+  if (r != CK_OK) return r;
+  if (T == 0) return ok();
+  r = check_logits(who, logits, lt);
+  if (r != CK_OK) return r;
+  if (!weights || !ids) return fail(CK_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(weights, 4) || !aligned(ids, 4)) return fail(CK_ERR_INVALID_ARG, "%s: misaligned output", who);
+  const int64_t grid = (T + ck::moe::kRouteWarps - 1) / ck::moe::kRouteWarps;
+  if (grid > INT32_MAX) return fail(CK_ERR_UNSUPPORTED, "%s: T=%lld too large", who, (long long)T);
+  const cudaError_t e = launch_pdl(ck::moe::route_kernel, dim3((unsigned)grid), dim3(32 * ck::moe::kRouteWarps), 0,
+                                   S(stream), logits, (int)lt, T, (int)E, top_k, renormalize, weights, ids);
+  if (e != cudaSuccess) return fail(CK_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  return launch_status(who);
+}
+
+size_t ck_moe_awq_w4a16_workspace_bytes(int64_t T, int top_k, int64_t I) {
+  return T <= 0 || top_k <= 0 || I <= 0 ? 0 : (size_t)T * (size_t)top_k * (size_t)I * 4;   // h as hi, lo
+}
+
+ck_status ck_moe_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_t K, int64_t I, int64_t E, int64_t ldx,
+                           int group_size, const void* logits, ck_dtype lt, int top_k, int renormalize,
+                           const uint8_t* gate_up_q, const void* gate_up_s, const void* gate_up_z,
+                           const uint8_t* down_q, const void* down_s, const void* down_z, void* out,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "moe_awq_w4a16";
+  ck_status r = check_choice(who, E, top_k);
+  if (r != CK_OK) return r;
+  if (T != 0) {
+    r = check_logits(who, logits, lt);
+    if (r != CK_OK) return r;
+  }
+  const ck::moe::Choice c = {logits, nullptr, nullptr, (int)lt, (int)T, (int)E, top_k, renormalize};
+  const MoeArgs a = {x, dt, T, K, I, E, ldx, group_size, gate_up_q, gate_up_s, gate_up_z,
+                     down_q, down_s, down_z, out, workspace, workspace_bytes};
+  return moe_impl(who, a, c, S(stream));
+}
+
+ck_status ck_moe_experts_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_t K, int64_t I, int64_t E,
+                                   int64_t ldx, int group_size, const int32_t* ids, const float* weights, int top_k,
+                                   const uint8_t* gate_up_q, const void* gate_up_s, const void* gate_up_z,
+                                   const uint8_t* down_q, const void* down_s, const void* down_z, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "moe_experts_awq_w4a16";
+  if (E <= 0 || top_k <= 0) return fail(CK_ERR_INVALID_ARG, "%s: E and top_k must be > 0", who);
+  if (E > ck::moe::kMaxExperts)
+    return fail(CK_ERR_UNSUPPORTED, "%s: E=%lld > %d", who, (long long)E, ck::moe::kMaxExperts);
+  if (top_k > ck::moe::kMaxTopK)
+    return fail(CK_ERR_UNSUPPORTED, "%s: top_k=%d > %d", who, top_k, ck::moe::kMaxTopK);
+  if (T != 0) {
+    if (!ids || !weights) return fail(CK_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!aligned(ids, 4) || !aligned(weights, 4))
+      return fail(CK_ERR_INVALID_ARG, "%s: misaligned ids or weights", who);
+  }
+  const ck::moe::Choice c = {nullptr, ids, weights, 0, (int)T, (int)E, top_k, 0};
+  const MoeArgs a = {x, dt, T, K, I, E, ldx, group_size, gate_up_q, gate_up_s, gate_up_z,
+                     down_q, down_s, down_z, out, workspace, workspace_bytes};
+  return moe_impl(who, a, c, S(stream));
+}
+
+size_t ck_lora_add_workspace_bytes(int64_t M, int64_t L) {
+  if (M <= ck::lora::kSelfGroup || L <= 0) return 0;
+  return (size_t)ck::lora::max_tiles(M, L, lora_tile(M, L)) * 16 + (size_t)M * 4;   // tile list, token order
+}
+
+ck_status ck_lora_add(const void* y, ck_dtype yt, const void* x, ck_dtype xt, int64_t M, int64_t K, int64_t N,
+                      int64_t R, int64_t L, int64_t ldx, int64_t ldy, int64_t ldo, const void* lora_a,
+                      const void* lora_b, const int32_t* ids, const float* scales, void* out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const char* who = "lora_add";
+  if (M < 0 || K <= 0 || N <= 0 || R <= 0 || L <= 0)
+    return fail(CK_ERR_INVALID_ARG, "%s: M must be >= 0, K, N, R and L > 0", who);
+  if (!known_float(xt) || !known_float(yt)) return fail(CK_ERR_INVALID_ARG, "%s: unknown dtype", who);
+  if (yt != CK_BF16 && yt != xt)
+    return fail(CK_ERR_UNSUPPORTED, "%s: y must be bf16 or of x's dtype", who);
+  if (R % 8 != 0 || R > 128) return fail(CK_ERR_UNSUPPORTED, "%s: R=%lld must be a multiple of 8, at most 128", who, (long long)R);
+  if (K % 8 != 0) return fail(CK_ERR_UNSUPPORTED, "%s: K=%lld must be a multiple of 8", who, (long long)K);
+  if (L > ck::lora::kMaxAdapters)
+    return fail(CK_ERR_UNSUPPORTED, "%s: L=%lld > %d", who, (long long)L, ck::lora::kMaxAdapters);
+  if (K > INT32_MAX / 2 || N > INT32_MAX / 2 || M > (int64_t)1 << 26)
+    return fail(CK_ERR_UNSUPPORTED, "%s: dimension too large", who);
+  if (M == 0) return ok();
+  if (ldx < K || ldx % 8 != 0)
+    return fail(CK_ERR_INVALID_ARG, "%s: ldx=%lld must be >= K and a multiple of 8", who, (long long)ldx);
+  if (ldy < N || ldo < N) return fail(CK_ERR_INVALID_ARG, "%s: ldy and ldo must be >= N", who);
+  if (!y || !x || !lora_a || !lora_b || !ids || !out) return fail(CK_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16))
+    return fail(CK_ERR_INVALID_ARG, "%s: x and the adapters must be 16-byte aligned", who);
+  if (!aligned(y, 2) || !aligned(out, 2) || !aligned(ids, 4) || (scales && !aligned(scales, 4)))
+    return fail(CK_ERR_INVALID_ARG, "%s: misaligned y, output, ids or scales", who);
+  const int64_t out_bytes = 2 * ((M - 1) * ldo + N);
+  if (!(out == y && ldo == ldy) && overlap(out, out_bytes, y, 2 * ((M - 1) * ldy + N)))
+    return fail(CK_ERR_INVALID_ARG, "%s: the output overlaps y without being y", who);
+  if (overlap(out, out_bytes, x, 2 * ((M - 1) * ldx + K)))
+    return fail(CK_ERR_INVALID_ARG, "%s: the output overlaps x", who);
+  using namespace ck::lora;
+  const int tm = lora_tile(M, L);
+  const int64_t tiles = max_tiles(M, L, tm);
+  ck::lora::Params p;
+  p.x = x; p.y = y; p.a = lora_a; p.b = lora_b; p.ids = ids; p.scales = scales; p.out = out;
+  p.ldx = ldx; p.ldy = ldy; p.ldo = ldo;
+  p.M = (int)M; p.K = (int)K; p.N = (int)N; p.R = (int)R; p.L = (int)L;
+  p.vec = N % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0 && aligned(y, 16) && aligned(out, 16);
+  p.tiles = nullptr;
+  p.order = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (M > kSelfGroup) {
+    const size_t need = ck_lora_add_workspace_bytes(M, L);
+    if (!workspace) return fail(CK_ERR_INVALID_ARG, "%s: null workspace", who);
+    if (!aligned(workspace, 256)) return fail(CK_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+    if (workspace_bytes < need)
+      return fail(CK_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
+    int32_t* tl = reinterpret_cast<int32_t*>(workspace);
+    int32_t* order = tl + 4 * tiles;
+    p.tiles = tl;
+    p.order = order;
+    e = launch_pdl(group_kernel, dim3(1), dim3(kGroupThreads), (size_t)(L + 1) * 4, S(stream), ids, (int)M, (int)L, tm,
+                   (int)tiles, tl, order);
+    if (e != cudaSuccess) return fail(CK_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  }
+  if (xt == CK_BF16) e = launch_lora<__nv_bfloat16, __nv_bfloat16>(p, tm, tiles, S(stream));
+  else if (yt == CK_FP16) e = launch_lora<__half, __half>(p, tm, tiles, S(stream));
+  else e = launch_lora<__half, __nv_bfloat16>(p, tm, tiles, S(stream));
+  if (e != cudaSuccess) return fail(CK_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  return launch_status(who);
+}
+
+}  // extern "C"

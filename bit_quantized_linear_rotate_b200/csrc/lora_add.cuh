@@ -1,0 +1,366 @@
+// Low-rank adapters of many requests beside a projection that all of them share.
+//
+//   out[m, :] = y[m, :] + scale[a] * ((x[m, :] A[a]^T) B[a]^T),   a = ids[m]
+//   out[m, :] = y[m, :]                                           where a is no adapter
+//
+// A tile is at most TM tokens of one adapter. A cluster of CTAs computes it in
+// one launch: each CTA multiplies its share of K (v = x A^T, the "shrink"), the
+// partial v are added through distributed shared memory in rank order, and
+// each CTA then multiplies all of v with its share of B's N rows and adds y (the
+// "expand"). v never goes to global memory. Both products are bound by bytes: x,
+// y and out once for each token, an adapter once for each of its tiles.
+//
+// Products are mma.sync.m16n8k16 with the tokens as the 16 rows of A. Their
+// operands come straight from global memory: a lane's 16 bytes are eight
+// consecutive k of one row, which serve as the k pairs of two MMAs (a sum over
+// k does not depend on how k is numbered). The columns of the expand's four
+// neighbouring MMAs are numbered so that a lane's results are eight consecutive
+// n of y: 16-byte loads and stores.
+//
+// v enters the expand as hi + lo of the inputs' 16-bit type, hi = round(v) and
+// lo = round(v - hi): what is lost is at most 2^-17 (bf16) or 2^-22 (fp16) of v. For
+// fp16 each row of v is first scaled by a power of two, which brings its
+// largest entry to [2^13, 2^14): v itself may lie outside fp16's range.
+//
+// A token's arithmetic does not depend on which tile it is in or which tokens
+// share that tile, so the order in which a batch is grouped does not show.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ck_common.cuh"
+#include "cluster_mem.cuh"
+#include "gemv_awq.cuh"
+
+namespace ck {
+namespace lora {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSelfGroup = 256;        // up to this many tokens a cluster finds its tile itself
+constexpr int kMaxAdapters = 8192;     // group_kernel counts them in shared memory
+constexpr int kGroupThreads = 1024;
+
+struct Params {
+  const void *x, *y, *a, *b;           // (M, K) T, (M, N) TY, (L, R, K) T, (L, N, R) T
+  const int32_t* ids;                  // (M)
+  const float* scales;                 // (L) or null
+  void* out;                           // (M, N) TY
+  int64_t ldx, ldy, ldo;
+  int M, K, N, R, L;
+  int vec;                             // y and out take 16-byte accesses
+  const int32_t* tiles;                // group_kernel's {adapter, start, count, 0} per tile, or null
+  const int32_t* order;                // its tokens in tile order
+};
+
+// Tiles of M tokens are at most this many, whatever the ids: full tiles, and one more for each
+// adapter (and for the tokens without one).
+__host__ __device__ inline int64_t max_tiles(int64_t M, int64_t L, int tm) {
+  const int64_t n = M / tm + L + 1;
+  return n < M ? n : M;
+}
+
+// Sorts the tokens of a large batch by adapter: tile list and token order, by one CTA. Bucket L
+// holds the tokens without an adapter.
+__global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __restrict__ ids, int M, int L, int tm,
+                                                              int max_tiles, int32_t* __restrict__ tiles,
+                                                              int32_t* __restrict__ order) {
+  extern __shared__ int32_t count[];                 // L + 1 counters, then each bucket's cursor
+  __shared__ int warp_sum[2][kGroupThreads / 32];
+  __shared__ int carry[2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i <= L; i += kGroupThreads) count[i] = 0;
+  if (tid == 0) carry[0] = carry[1] = 0;
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  for (int i = tid; i < (M + 31) / 32 * 32; i += kGroupThreads) {
+    int a = i < M ? ids[i] : -2;
+    if (i < M && (a < 0 || a >= L)) a = L;
+    const unsigned same = __match_any_sync(0xffffffffu, a);
+    if (a >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[a], __popc(same));
+  }
+  __syncthreads();
+  for (int b0 = 0; b0 <= L; b0 += kGroupThreads) {   // running sums of tokens and of tiles
+    const int b = b0 + tid;
+    const int n = b <= L ? count[b] : 0, nt = (n + tm - 1) / tm;
+    int in = n, it = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int un = __shfl_up_sync(0xffffffffu, in, o), ut = __shfl_up_sync(0xffffffffu, it, o);
+      if (lane >= o) in += un, it += ut;
+    }
+    if (lane == 31) warp_sum[0][warp] = in, warp_sum[1][warp] = it;
+    __syncthreads();
+    int bn = carry[0], bt = carry[1];
+    for (int w = 0; w < warp; ++w) bn += warp_sum[0][w], bt += warp_sum[1][w];
+    const int start = bn + in - n;
+    int tile = bt + it - nt;
+    if (b <= L) {
+      count[b] = start;
+      for (int s = 0; s < n; s += tm, ++tile) {
+        int4 v = make_int4(b < L ? b : -1, start + s, min(tm, n - s), 0);
+        reinterpret_cast<int4*>(tiles)[tile] = v;
+      }
+    }
+    __syncthreads();
+    if (tid == kGroupThreads - 1) carry[0] = bn + in, carry[1] = bt + it;
+    __syncthreads();
+  }
+  for (int i = carry[1] + tid; i < max_tiles; i += kGroupThreads)   // tiles that this batch has not
+    reinterpret_cast<int4*>(tiles)[i] = make_int4(-1, 0, 0, 0);
+  for (int i = tid; i < (M + 31) / 32 * 32; i += kGroupThreads) {
+    int a = i < M ? ids[i] : -2;
+    if (i < M && (a < 0 || a >= L)) a = L;
+    const unsigned same = __match_any_sync(0xffffffffu, a);
+    const int leader = __ffs(same) - 1;
+    int at = 0;
+    if (a >= 0 && lane == leader) at = atomicAdd(&count[a], __popc(same));
+    at = __shfl_sync(0xffffffffu, at, leader);
+    if (a >= 0) order[at + __popc(same & ((1u << lane) - 1))] = i;
+  }
+}
+
+// This cluster's tile: adapter (-1: none) and tokens; returns their number (0: no such tile).
+template <int TM>
+__device__ __forceinline__ int find_tile(const Params& p, int tile, int (&token)[TM], int& adapter, int* scratch) {
+  const int tid = threadIdx.x;
+  if (p.tiles != nullptr) {
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(p.tiles) + tile);
+    if (tid < v.z) token[tid] = __ldcg(p.order + v.y + tid);
+    adapter = v.x;
+    __syncthreads();
+    return v.z;
+  }
+  // M <= 256 = kThreads: token i's rank among the tokens of its adapter; every TM-th begins a
+  // tile, and tiles are numbered by their first tokens.
+  int* id = scratch;                                  // [kSelfGroup]
+  int* found = scratch + kSelfGroup;                  // adapter, rank of the tile's first token, count
+  int a = -2;
+  if (tid < p.M) {
+    a = p.ids[tid];
+    if (a < 0 || a >= p.L) a = -1;
+  }
+  id[tid] = a;
+  if (tid == 0) found[0] = -1, found[1] = 0, found[2] = 0;
+  __syncthreads();
+  int rank = 0;
+  if (tid < p.M)
+    for (int j = 0; j < tid; ++j) rank += id[j] == a;
+  const bool first = tid < p.M && rank % TM == 0;
+  const int before = __popc(__ballot_sync(0xffffffffu, first) & ((1u << (tid & 31)) - 1));
+  int* warp_n = found + 4;
+  if ((tid & 31) == 31) warp_n[tid >> 5] = before + (first ? 1 : 0);
+  __syncthreads();
+  int number = before;
+  for (int w = 0; w < (tid >> 5); ++w) number += warp_n[w];
+  if (first && number == tile) found[0] = a, found[1] = rank, found[2] = 1;
+  __syncthreads();
+  const bool any = found[2] != 0;
+  const int fa = found[0], fr = found[1];
+  const bool mine = any && tid < p.M && a == fa && rank >= fr && rank < fr + TM;
+  if (mine) token[rank - fr] = tid;
+  adapter = fa;
+  return __syncthreads_count(mine);
+}
+
+template <typename T> struct Half2Of;
+template <> struct Half2Of<__nv_bfloat16> { static constexpr bool kScaled = false; };
+template <> struct Half2Of<__half> { static constexpr bool kScaled = true; };
+
+// Shared memory of a CTA: RC 32-wide chunks of rank, TM tokens.
+template <int RC, int TM>
+struct Smem {
+  static constexpr int kR = 32 * RC;
+  static constexpr int kVStride = kR + 8;             // 16-bit elements: rows 16 bytes apart in the banks
+  static constexpr int kSplit = kWarps / (TM / 16);   // warps that share an m16 tile in the shrink
+  float part[kSplit][TM][kR];                         // the warps' sums; [0]: this CTA's
+  float v[TM][kR];                                    // the cluster's
+  uint16_t hi[TM][kVStride], lo[TM][kVStride];
+  float row_scale[TM];
+  int token[TM];
+  int scratch[kSelfGroup + 16];
+};
+
+template <typename T, typename TY, int RC, int TM>
+__global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  using SM = Smem<RC, TM>;
+  using Tr = awq::Traits<T>;
+  SM& S = *reinterpret_cast<SM*>(sm);
+  constexpr int MT = TM / 16, KS = SM::kSplit, RT = 4 * RC;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
+  grid_dep_wait();
+  grid_dep_launch();
+  int adapter;
+  const int n = find_tile<TM>(p, (int)(blockIdx.x / ranks), S.token, adapter, S.scratch);
+  if (n == 0) return;                                 // the same for all CTAs of the cluster
+  const T* x = reinterpret_cast<const T*>(p.x);
+  const TY* y = reinterpret_cast<const TY*>(p.y);
+  TY* out = reinterpret_cast<TY*>(p.out);
+  const int nb = (p.N + 31) / 32;                     // blocks of 32 columns
+  const int nb0 = (int)((int64_t)nb * rank / ranks), nb1 = (int)((int64_t)nb * (rank + 1) / ranks);
+
+  if (adapter < 0) {                                  // tokens without an adapter
+    if (y != out) {
+      const int c0 = 32 * nb0, c1 = min(32 * nb1, p.N);
+      for (int m = warp; m < n; m += kWarps) {
+        const TY* yp = y + S.token[m] * p.ldy;
+        TY* op = out + S.token[m] * p.ldo;
+        if (p.vec)
+          for (int c = c0 + 8 * lane; c < c1; c += 256)
+            *reinterpret_cast<uint4*>(op + c) = *reinterpret_cast<const uint4*>(yp + c);
+        else
+          for (int c = c0 + lane; c < c1; c += 32) op[c] = yp[c];
+      }
+    }
+    return;
+  }
+
+  // ---- shrink: part = x A^T over this warp's share of k
+  {
+    const int mt = warp % MT, ks = warp / MT;
+    const int nk = (p.K + 31) / 32;
+    const int kc0 = (int)((int64_t)nk * (rank * KS + ks) / (ranks * KS));
+    const int kc1 = (int)((int64_t)nk * (rank * KS + ks + 1) / (ranks * KS));
+    const int m0 = 16 * mt + g, m1 = m0 + 8;
+    const T* x0 = m0 < n ? x + S.token[m0] * p.ldx + 8 * t : nullptr;
+    const T* x1 = m1 < n ? x + S.token[m1] * p.ldx + 8 * t : nullptr;
+    const T* ap = reinterpret_cast<const T*>(p.a) + ((int64_t)adapter * p.R + g) * p.K + 8 * t;
+    float c[RT][4] = {};
+    if (16 * mt < n) {
+#pragma unroll 2
+      for (int kc = kc0; kc < kc1; ++kc) {
+        const int k = 32 * kc;
+        const bool in = k + 8 * t < p.K;              // K % 8 == 0: all eight or none
+        uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;
+        if (in && x0 != nullptr) q0 = *reinterpret_cast<const uint4*>(x0 + k);
+        if (in && x1 != nullptr) q1 = *reinterpret_cast<const uint4*>(x1 + k);
+        const uint32_t fa[4] = {q0.x, q1.x, q0.y, q1.y}, fb[4] = {q0.z, q1.z, q0.w, q1.w};
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          if (8 * j >= p.R) break;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (in) w = __ldg(reinterpret_cast<const uint4*>(ap + (int64_t)8 * j * p.K + k));
+          Tr::mma(c[j], fa, w.x, w.y);
+          Tr::mma(c[j], fb, w.z, w.w);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      *reinterpret_cast<float2*>(&S.part[ks][m0][8 * j + 2 * t]) = make_float2(c[j][0], c[j][1]);
+      *reinterpret_cast<float2*>(&S.part[ks][m1][8 * j + 2 * t]) = make_float2(c[j][2], c[j][3]);
+    }
+  }
+  __syncthreads();
+  constexpr int kCells = TM * SM::kR;
+  float* part = &S.part[0][0][0];
+  for (int i = tid; i < kCells; i += kThreads) {
+    float s = part[i];
+#pragma unroll
+    for (int w = 1; w < KS; ++w) s += part[w * kCells + i];
+    part[i] = s;
+  }
+  // each CTA adds its share of the cells over the ranks and hands the sums to all
+  cluster_sync();
+  const uint32_t part_at = smem_u32(part), v_at = smem_u32(&S.v[0][0]);
+  for (int i = rank * kThreads + tid; i < kCells; i += ranks * kThreads) {
+    float s = 0.0f;
+    for (int r = 0; r < ranks; ++r) s += ld_cluster_f32(mapa_shared(part_at + 4 * i, r));
+    for (int r = 0; r < ranks; ++r) st_cluster_f32(mapa_shared(v_at + 4 * i, r), s);
+  }
+  cluster_sync();
+
+  // ---- v as hi + lo
+  const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
+  for (int m = warp; m < TM; m += kWarps) {
+    float v[RC];
+    int ex = 0;
+#pragma unroll
+    for (int i = 0; i < RC; ++i) v[i] = S.v[m][32 * i + lane];
+    if constexpr (Half2Of<T>::kScaled) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < RC; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+      top = __reduce_max_sync(0xffffffffu, top) >> 23;              // the largest exponent
+      if (top > 0 && top < 255) ex = max(-100, min(100, 13 - ((int)top - 127)));
+    }
+    const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+    for (int i = 0; i < RC; ++i) {
+      const float s = v[i] * up;
+      const T h = Tr::fromf(s);
+      const float hf = Tr::tof(h);
+      const T l = Tr::fromf(isfinite(hf) ? s - hf : 0.0f);          // an infinity stays one
+      S.hi[m][32 * i + lane] = *reinterpret_cast<const uint16_t*>(&h);
+      S.lo[m][32 * i + lane] = *reinterpret_cast<const uint16_t*>(&l);
+    }
+    if (lane == 0) S.row_scale[m] = as * __uint_as_float((uint32_t)(127 - ex) << 23);
+  }
+  __syncthreads();
+
+  // ---- expand: out = y + row_scale * (v B^T), 32 columns at a time
+  const T* b = reinterpret_cast<const T*>(p.b) + (int64_t)adapter * p.N * p.R + 8 * t;
+  for (int blk = nb0 + warp; blk < nb1; blk += kWarps) {
+    const int c0 = 32 * blk;
+    float c[MT][4][4] = {};
+#pragma unroll
+    for (int rc = 0; rc < RC; ++rc) {
+      if (32 * rc >= p.R) break;
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
+        w[j] = make_uint4(0, 0, 0, 0);
+        if (col < p.N && 32 * rc + 8 * t < p.R) w[j] = __ldg(reinterpret_cast<const uint4*>(b + (int64_t)col * p.R + 32 * rc));
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (16 * mt >= n) break;
+        const int m0 = 16 * mt + g, at = 32 * rc + 8 * t;
+        const uint4 h0 = *reinterpret_cast<const uint4*>(&S.hi[m0][at]), h1 = *reinterpret_cast<const uint4*>(&S.hi[m0 + 8][at]);
+        const uint4 l0 = *reinterpret_cast<const uint4*>(&S.lo[m0][at]), l1 = *reinterpret_cast<const uint4*>(&S.lo[m0 + 8][at]);
+        const uint32_t ha[4] = {h0.x, h1.x, h0.y, h1.y}, hb[4] = {h0.z, h1.z, h0.w, h1.w};
+        const uint32_t la[4] = {l0.x, l1.x, l0.y, l1.y}, lb[4] = {l0.z, l1.z, l0.w, l1.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          Tr::mma(c[mt][j], ha, w[j].x, w[j].y);
+          Tr::mma(c[mt][j], hb, w[j].z, w[j].w);
+          Tr::mma(c[mt][j], la, w[j].x, w[j].y);
+          Tr::mma(c[mt][j], lb, w[j].z, w[j].w);
+        }
+      }
+    }
+    using TrY = awq::Traits<TY>;
+    const int col = c0 + 8 * t;                       // this lane's eight columns
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int m = 16 * mt + g + 8 * hf;
+        if (m >= n || col >= p.N) continue;
+        const float f = S.row_scale[m];
+        const TY* yp = y + S.token[m] * p.ldy + col;
+        TY* op = out + S.token[m] * p.ldo + col;
+        TY e[8];
+        if (p.vec) {
+          *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(yp);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            e[i] = TrY::fromf(fmaf(f, c[mt][i >> 1][2 * hf + (i & 1)], TrY::tof(e[i])));
+          *reinterpret_cast<uint4*>(op) = *reinterpret_cast<const uint4*>(e);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (col + i < p.N) op[i] = TrY::fromf(fmaf(f, c[mt][i >> 1][2 * hf + (i & 1)], TrY::tof(yp[i])));
+        }
+      }
+  }
+}
+
+}  // namespace lora
+}  // namespace ck

@@ -1,0 +1,231 @@
+// Expert routing: the k largest of each token's logits, their softmax weights,
+// and, inside one CTA, the lists of tokens that each expert gets.
+//
+//   chosen_t = the k live entries of l[t, :] that come first in (value
+//              descending, index ascending); live means l > -inf (a NaN is not)
+//   w[t, j]  = exp(l[t, c_j] - m_t) / S_t,  m_t = max_e l[t, e],
+//              S_t = the sum of those exponentials over the chosen entries
+//              (renormalised) or over all live ones
+//
+// A slot without a live entry gets the id -1 and the weight 0. Where m_t is
+// +inf the limit is taken: the +inf entries share the weight equally.
+//
+// One warp handles one token. Every logit becomes an unsigned key that sorts as
+// the value does (0 for entries that are not live), so a round of the choice
+// is one redux.max over the keys and one redux.min over the indices of those
+// that hold it: ties go to the lowest index, and no value is rounded.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ck_common.cuh"
+
+namespace ck {
+namespace moe {
+
+constexpr int kMaxExperts = 512;
+constexpr int kMaxTopK = 16;
+constexpr int kMaxTokens = 64;                       // of the experts' kernels; ck_moe_route takes any number
+constexpr int kMaxSlots = kMaxTokens * kMaxTopK;
+constexpr int kLogitBf16 = 0, kLogitFp16 = 1, kLogitFp32 = 2;   // = ck_dtype
+
+// Read past L1: a dependent kernel may read the logits before its own
+// dependency wait (down_kernel), when this SM's L1 need not hold them yet.
+__device__ __forceinline__ float load_logit(const void* p, int dt, int64_t i) {
+  if (dt == kLogitFp32) return __ldcg(reinterpret_cast<const float*>(p) + i);
+  const unsigned short u = __ldcg(reinterpret_cast<const unsigned short*>(p) + i);
+  if (dt == kLogitBf16) return __uint_as_float((uint32_t)u << 16);
+  return __half2float(__ushort_as_half(u));
+}
+
+// Unsigned key in the order of the values; 0 for an entry that is not live.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);      // -0 counts as +0
+  const uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
+  return v > -INFINITY ? key : 0u;
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key >> 31) ? (key & 0x7fffffffu) : ~key);
+}
+
+// exp(v - m) with the limit at m = +inf.
+__device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.0f : expf(v - m); }
+
+// The choice for one token by one warp, V logits a lane (E <= 32 V; lane l
+// holds the entries l, l + 32, ...). Lane j < k returns slot j's id and weight.
+template <int V>
+__device__ __forceinline__ void choose(const void* logits, int ldt, int64_t row, int E, int k, bool renorm, int& id,
+                                       float& w) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < E ? order_key(load_logit(logits, ldt, row * E + e)) : 0u;
+  }
+  uint32_t all[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) all[i] = key[i];
+  int my_id = -1;
+  uint32_t my_key = 0u, top = 0u;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    if (m == 0u) break;                              // no live entry is left
+    uint32_t at = 0xffffffffu;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] == m) at = (uint32_t)(lane + 32 * i);
+    at = __reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if ((uint32_t)(lane + 32 * i) == at) key[i] = 0u;
+    if (j == 0) top = m;
+    if (lane == j) {
+      my_id = (int)at;
+      my_key = m;
+    }
+  }
+  const float mv = key_value(top);
+  const float p = my_id >= 0 ? exp_below(key_value(my_key), mv) : 0.0f;
+  float s = 0.0f;
+  if (renorm) {
+    s = p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (all[i] != 0u) s += exp_below(key_value(all[i]), mv);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  id = my_id;
+  w = my_id >= 0 ? p / s : 0.0f;
+}
+
+__device__ __forceinline__ void choose_any(const void* logits, int ldt, int64_t row, int E, int k, bool renorm,
+                                           int& id, float& w) {
+  if (E <= 128) choose<4>(logits, ldt, row, E, k, renorm, id, w);
+  else choose<16>(logits, ldt, row, E, k, renorm, id, w);
+}
+
+constexpr int kRouteWarps = 4;
+
+// One warp per token.
+__global__ void __launch_bounds__(kRouteWarps * 32)
+    route_kernel(const void* logits, int ldt, int64_t T, int E, int k, int renorm, float* __restrict__ weights,
+                 int32_t* __restrict__ ids) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= T) return;
+  int id;
+  float w;
+  choose_any(logits, ldt, t, E, k, renorm != 0, id, w);
+  const int lane = threadIdx.x & 31;
+  if (lane < k) {
+    weights[t * k + lane] = w;
+    ids[t * k + lane] = id;
+  }
+}
+
+// Where a layer's choice comes from: logits (ids == nullptr), or given ids and
+// weights of shape (T, k).
+struct Choice {
+  const void* logits;
+  const int32_t* ids;
+  const float* weights;
+  int ldt, T, E, k, renorm;
+};
+
+// The experts' token lists of a batch of at most kMaxTokens tokens, in shared
+// memory. The slots that some token fills are numbered by (expert, token); a
+// unit is at most `cap` consecutive slots of one expert.
+struct Lists {
+  unsigned long long mask[kMaxExperts];              // tokens of each expert
+  float w[kMaxSlots];                                // the choice as given
+  int16_t id[kMaxSlots];
+  float slot_w[kMaxSlots];
+  uint8_t slot_token[kMaxSlots];
+  uint16_t unit_expert[kMaxSlots];
+  uint16_t unit_start[kMaxSlots];
+  uint8_t unit_n[kMaxSlots];
+  int warp_sum[32];
+  int n_units;
+};
+
+// Fills L from the choice, by all THREADS threads of the CTA (2 THREADS >=
+// kMaxExperts); the lists may be read after the closing barrier. An expert
+// that a token names twice gets it once, with the sum of the two weights. The
+// order is fixed, so every CTA of both kernels builds the same lists.
+template <int THREADS>
+__device__ __forceinline__ void build_lists(const Choice& c, Lists& L, int cap) {
+  static_assert(2 * THREADS >= kMaxExperts, "two experts a thread");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int e = tid; e < c.E; e += THREADS) L.mask[e] = 0ull;
+  const int slots = c.T * c.k;
+  if (c.ids == nullptr) {
+    for (int t = warp; t < c.T; t += THREADS / 32) {
+      int id;
+      float w;
+      choose_any(c.logits, c.ldt, t, c.E, c.k, c.renorm != 0, id, w);
+      if (lane < c.k) {
+        L.id[t * c.k + lane] = (int16_t)id;
+        L.w[t * c.k + lane] = w;
+      }
+    }
+  } else {
+    for (int s = tid; s < slots; s += THREADS) {
+      const int id = __ldcg(c.ids + s);
+      L.id[s] = (int16_t)(id >= 0 && id < c.E ? id : -1);
+      L.w[s] = __ldcg(c.weights + s);
+    }
+  }
+  __syncthreads();
+  for (int s = tid; s < slots; s += THREADS)
+    if (L.id[s] >= 0) atomicOr(&L.mask[L.id[s]], 1ull << (s / c.k));
+  __syncthreads();
+  int n[2], v = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * tid + i;
+    n[i] = e < c.E ? __popcll(L.mask[e]) : 0;
+    v += ((n[i] + cap - 1) / cap) << 16 | n[i];      // units and slots in one word: both at most kMaxSlots
+  }
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) L.warp_sum[warp] = incl;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < warp; ++i) before += L.warp_sum[i];
+  int unit = (before + incl - v) >> 16, slot = (before + incl - v) & 0xffff;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (n[i] == 0) continue;
+    const int e = 2 * tid + i;
+    for (int s = 0; s < n[i]; s += cap, ++unit) {
+      L.unit_expert[unit] = (uint16_t)e;
+      L.unit_start[unit] = (uint16_t)(slot + s);
+      L.unit_n[unit] = (uint8_t)min(cap, n[i] - s);
+    }
+    for (unsigned long long m = L.mask[e]; m != 0ull; m &= m - 1, ++slot) {
+      const int t = __ffsll((long long)m) - 1;
+      float w = 0.0f;
+      for (int j = 0; j < c.k; ++j)
+        if (L.id[t * c.k + j] == e) w += L.w[t * c.k + j];
+      L.slot_token[slot] = (uint8_t)t;
+      L.slot_w[slot] = w;
+    }
+  }
+  if (tid == THREADS - 1) L.n_units = (before + incl) >> 16;
+  __syncthreads();
+}
+
+}  // namespace moe
+}  // namespace ck

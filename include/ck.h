@@ -56,7 +56,7 @@ typedef enum {
   CK_ERR_TIMEOUT = 4
 } ck_status;
 
-typedef enum { CK_BF16 = 0, CK_FP16 = 1 } ck_dtype;
+typedef enum { CK_BF16 = 0, CK_FP16 = 1, CK_FP32 = 2 /* router logits only */ } ck_dtype;
 
 /*
  * Fused group rotation + rowwise symmetric quantization
@@ -378,6 +378,89 @@ ck_status ck_gemv_w4a8_tc(const int8_t* xq, const float* x_scale, int64_t M, int
 ck_status ck_gemv_awq_w4a16(const void* x, ck_dtype dt, int64_t M, int64_t K, int64_t N,
                             int group_size, const uint8_t* qweight, const void* wscales,
                             const void* wzeros, const void* bias, void* y, void* stream);
+
+/*
+ * Expert routing: the top_k largest of each token's logits and their softmax
+ * weights.
+ * logits  : (T, E) bf16, fp16 or fp32 (lt).
+ * weights : (T, top_k) float32, ids : (T, top_k) int32, in descending order of
+ *           the logits; equal logits go to the lowest index first.
+ * The weight of a chosen expert is exp(l - m) / S, m the row's largest logit and
+ * S the sum of these exponentials over the chosen experts (renormalize != 0) or
+ * over all experts (renormalize == 0).
+ * A logit of -inf or NaN is never chosen and has no share; a slot for which no
+ * logit is left gets id -1 and weight 0. Where the largest logit is +inf, the
+ * +inf logits share the weight equally.
+ * T may be any number (0: no-op); E <= 512, top_k <= 16, top_k <= E.
+ */
+ck_status ck_moe_route(const void* logits, ck_dtype lt, int64_t T, int64_t E, int top_k,
+                       int renormalize, float* weights, int32_t* ids, void* stream);
+
+/*
+ * A mixture-of-experts layer for up to 64 tokens whose experts are in the AWQ
+ * W4A16 format of ck_gemv_awq_w4a16:
+ *   W[n,k]  = (u[n,k] - 8) * s[k/G, n] + z[k/G, n]        (each expert's)
+ *   h       = silu(x Wgate^T) * (x Wup^T)                 (float32 accumulation)
+ *   out[t]  = sum over t's experts of weight * (h Wdown^T)
+ * rounded once, to dt. Two kernels; the weights of an expert are read once,
+ * and only of experts that some token goes to.
+ * dt applies to x, the scales, the zeros and out (bf16 or fp16).
+ * x         : (T, K), row stride ldx >= K elements, ldx % 8 == 0; 0 <= T <= 64.
+ * gate_up_q : (E, 2 I, K/2) packed uint4, each expert's I gate rows, then its
+ *             I up rows; gate_up_s, gate_up_z : (E, K/G, 2 I).
+ * down_q    : (E, K, I/2); down_s, down_z : (E, I/G, K).
+ * out       : (T, K) contiguous; may be x itself (ldx == K), must not overlap
+ *             the workspace or other inputs.
+ * group_size G : 64, 128 or 256, and a divisor of K and I.
+ * x, the weights, scales and zeros are 16-byte aligned; the workspace is
+ * 256-byte aligned, at least ck_moe_awq_w4a16_workspace_bytes(T, top_k, I)
+ * bytes, and belongs to the call until it has run.
+ * ck_moe_awq_w4a16 routes by itself, as ck_moe_route does with logits, lt,
+ * top_k and renormalize. ck_moe_experts_awq_w4a16 takes the choice: ids and
+ * weights of shape (T, top_k). There a slot whose id lies outside [0, E) is empty,
+ * and an expert that a token names twice counts with the sum of its weights.
+ * A token without an expert gets zeros. A token with an activation that is not
+ * finite gets outputs that are not finite (NaN in general); other tokens are
+ * not affected. The result does not depend on timing.
+ */
+size_t ck_moe_awq_w4a16_workspace_bytes(int64_t T, int top_k, int64_t I);
+ck_status ck_moe_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_t K, int64_t I, int64_t E,
+                           int64_t ldx, int group_size, const void* logits, ck_dtype lt, int top_k,
+                           int renormalize, const uint8_t* gate_up_q, const void* gate_up_s,
+                           const void* gate_up_z, const uint8_t* down_q, const void* down_s,
+                           const void* down_z, void* out, void* workspace, size_t workspace_bytes,
+                           void* stream);
+ck_status ck_moe_experts_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_t K, int64_t I,
+                                   int64_t E, int64_t ldx, int group_size, const int32_t* ids,
+                                   const float* weights, int top_k, const uint8_t* gate_up_q,
+                                   const void* gate_up_s, const void* gate_up_z,
+                                   const uint8_t* down_q, const void* down_s, const void* down_z,
+                                   void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Low-rank adapters of many requests, added to the output of a projection that
+ * all of them share (any linear of this library):
+ *   out[m] = y[m] + scales[a] * ((x[m] A[a]^T) B[a]^T),   a = ids[m]
+ *   out[m] = y[m]                                         where a is outside [0, L)
+ * in float32, rounded once, to yt.
+ * x      : (M, K) bf16 or fp16 (xt), row stride ldx >= K, ldx % 8 == 0.
+ * y, out : (M, N), bf16 or xt (yt), row strides ldy, ldo >= N elements. out may be
+ *          y itself with the same stride; otherwise it must not overlap y, and
+ *          never x. Rows that start on 16-byte boundaries with N % 8 == 0 are the
+ *          fast case; any other N and stride works.
+ * lora_a : (L, R, K) xt, lora_b : (L, N, R) xt, contiguous, 16-byte aligned. Adapters
+ *          of lower rank are padded with zeros.
+ * ids    : (M) int32, any order. scales : (L) float32, or NULL for 1.
+ * R a multiple of 8 up to 128, K % 8 == 0, L <= 8192, M <= 2^26 (0: no-op).
+ * workspace : at least ck_lora_add_workspace_bytes(M, L) bytes, 256-byte aligned
+ *          (NULL where that is 0), belongs to the call until it has run.
+ */
+size_t ck_lora_add_workspace_bytes(int64_t M, int64_t L);
+ck_status ck_lora_add(const void* y, ck_dtype yt, const void* x, ck_dtype xt, int64_t M, int64_t K,
+                      int64_t N, int64_t R, int64_t L, int64_t ldx, int64_t ldy, int64_t ldo,
+                      const void* lora_a, const void* lora_b, const int32_t* ids,
+                      const float* scales, void* out, void* workspace, size_t workspace_bytes,
+                      void* stream);
 
 /*
  * Test hooks: raw int32 accumulators acc[m,n] = sum_k qa[m,k] * w[n,k] through

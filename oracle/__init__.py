@@ -6,7 +6,11 @@ only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` /
 code, tables or helpers with the CUDA library under
 ``bit_quantized_linear_rotate_b200/csrc``.
 
-Every function is a plain, slow, obviously-correct restatement of what the
+Beside the pages' path it holds the operators whose weights are chosen for each
+token (``oracle/chosen.py``: expert routing, the mixture-of-experts layer on AWQ
+experts, per-request low-rank adapters), from their formulas.
+
+Every other function is a plain, slow, obviously-correct restatement of what the
 pages define, in float64 wherever the pages leave the precision open:
 
 * the groupwise Hadamard rotation and rowwise symmetric quantization of
@@ -27,6 +31,7 @@ against closed forms, invariants, brute force or hand-worked fixtures under
 pages do not fix it); it is pinned only through the 1e-2 output tolerance.
 """
 
+from .chosen import lora_add, moe_awq_w4a16, moe_route, silu  # noqa: F401
 from .convrot import (  # noqa: F401
     QMAX,
     awq_dequantize,
