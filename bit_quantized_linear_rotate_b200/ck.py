@@ -60,7 +60,7 @@ SIGNATURES = {
     "ck_gemv_w4a8_tc": [_p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p],
     "ck_gemv_awq_w4a16": [_p, _int, _i64, _i64, _i64, _int, _p, _p, _p, _p, _p, _p],
     "ck_moe_route": [_p, _int, _i64, _i64, _int, _int, _p, _p, _p],
-    "ck_moe_awq_w4a16_workspace_bytes": [_i64, _int, _i64],
+    "ck_moe_awq_w4a16_workspace_bytes": [_i64, _int, _i64, _i64],
     "ck_moe_awq_w4a16": [_p, _int, _i64, _i64, _i64, _i64, _i64, _int, _p, _int, _int, _int, _p, _p, _p, _p, _p, _p,
                          _p, _p, ctypes.c_size_t, _p],
     "ck_moe_experts_awq_w4a16": [_p, _int, _i64, _i64, _i64, _i64, _i64, _int, _p, _p, _int, _p, _p, _p, _p, _p, _p,
@@ -500,8 +500,8 @@ def moe_route(logits, top_k: int, renormalize: bool = True, weights_out=None, id
     return weights, ids
 
 
-def moe_awq_w4a16_workspace_bytes(T: int, top_k: int, I: int) -> int:
-    return int(lib.ck_moe_awq_w4a16_workspace_bytes(T, top_k, I))
+def moe_awq_w4a16_workspace_bytes(T: int, top_k: int, K: int, I: int) -> int:
+    return int(lib.ck_moe_awq_w4a16_workspace_bytes(T, top_k, K, I))
 
 
 def _moe(name, x, given, choice, top_k, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, group_size, workspace, out,
@@ -524,7 +524,7 @@ def _moe(name, x, given, choice, top_k, gate_up_q, gate_up_s, gate_up_z, down_q,
                down_s=(down_s, (E, I // G, K)), down_z=(down_z, (E, I // G, K)), out=(out, (T, K)))
     dev = _cuda(x, *given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, workspace, out)
     if workspace is None:
-        workspace = _empty((moe_awq_w4a16_workspace_bytes(T, top_k, I),), torch.uint8, dev, stream)
+        workspace = _empty((moe_awq_w4a16_workspace_bytes(T, top_k, K, I),), torch.uint8, dev, stream)
     if out is None:
         out = _empty((T, K), x.dtype, dev, stream)
     _call(dev, "ck_" + name, x.data_ptr(), _dtype_code(x.dtype), T, K, I, E, _ld(x), G, *choice, gate_up_q.data_ptr(),

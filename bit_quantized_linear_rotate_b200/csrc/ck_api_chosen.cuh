@@ -53,42 +53,101 @@ ck_status check_logits(const char* who, const void* logits, ck_dtype lt) {
 
 // -------------------------------------------------------- mixture of experts
 
-template <typename T, int NT>
-cudaError_t launch_gate_up(const ck::moe::Params& p, cudaStream_t st) {
+template <typename T, int NT, bool SELF>
+cudaError_t launch_gate_up(const ck::moe::Maps& maps, const ck::moe::Params& p, cudaStream_t st) {
   using namespace ck::moe;
-  auto kern = gate_up_kernel<T, NT>;
+  auto kern = gate_up_kernel<T, NT, SELF>;
   struct Tag {};
-  const cudaError_t e = set_smem_max<Tag>(kern, (int)sizeof(GateUpSmem<NT>));
+  const int sums = gate_up_sums<NT>() + (SELF ? self_bytes(p.choice.T, p.K) : 0);
+  const int stages = ring_stages(sums, kStreamSmemMax);
+  static_assert(ring_stages(gate_up_sums<NT>() + (SELF ? self_bytes(1, kSelfX) : 0), kStreamSmemMax) >= 2,
+                "two stages at least");
+  const int smem = 1024 + ring_offset(sums) + stages * kStage;
+  const cudaError_t e = set_smem_max<Tag>(kern, smem);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)p.choice.T * p.choice.k * (p.I / kColsItem);   // a unit has a slot at least
   const unsigned grid = (unsigned)std::min<int64_t>(most, 2 * sm_count());
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), sizeof(GateUpSmem<NT>), st, p);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, maps, p, stages);
 }
 
 template <typename T, int NT>
-cudaError_t launch_down(const ck::moe::Params& p, cudaStream_t st) {
+cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cudaStream_t st) {
   using namespace ck::moe;
   auto kern = down_kernel<T, NT>;
   struct Tag {};
-  const size_t smem = sizeof(DownSmem) + (size_t)kWarps * p.choice.T * kRowsTile * 4;
-  const cudaError_t e = set_smem_max<Tag>(kern, (int)smem);
+  const int sums = down_sums(p.choice.T), stages = ring_stages(sums, kStreamSmemMax);
+  static_assert(ring_stages(down_sums(kMaxTokens), kStreamSmemMax) >= 2, "two stages at least");
+  const int smem = 1024 + ring_offset(sums) + stages * kStage;
+  const cudaError_t e = set_smem_max<Tag>(kern, smem);
   if (e != cudaSuccess) return e;
   const int tiles = p.K / kRowsTile;
   int cs = 8;
   while (cs > 1 && tiles * cs > 2 * sm_count()) cs /= 2;
-  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kThreads, smem, st, p);
+  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kThreads, smem, st, maps, p, stages);
 }
 
+// Workspace: x as fixed point, h as fixed point, the choice (prepare_kernel's).
+struct MoeWorkspace {
+  size_t xq, xs, hq, hs, ids, weights, total;
+  MoeWorkspace(int64_t T, int k, int64_t K, int64_t I) {
+    size_t at = 0;
+    auto take = [&at](int64_t bytes) {
+      const size_t a = at;
+      at = (at + (size_t)bytes + 255) / 256 * 256;
+      return a;
+    };
+    xq = take(T * K * 2);
+    xs = take(T * (K / 64) * 8);
+    hq = take(T * k * I * 2);
+    hs = take(T * k * (I / 64) * 8);
+    ids = take(T * k * 4);
+    weights = take(T * k * 4);
+    total = at;
+  }
+};
+
 template <typename T>
-cudaError_t launch_moe(const ck::moe::Params& p, cudaStream_t st) {
+cudaError_t launch_moe(const ck::moe::Maps& gate_up, const ck::moe::Maps& down, ck::moe::Params& p, uint8_t* ws,
+                       const MoeWorkspace& w, cudaStream_t st) {
+  using namespace ck::moe;
+  const int tokens = p.choice.T;
   cudaError_t e;
-  if (p.choice.T <= 8) e = launch_gate_up<T, 1>(p, st);
-  else if (p.choice.T <= 16) e = launch_gate_up<T, 2>(p, st);
-  else e = launch_gate_up<T, 4>(p, st);
+  if (tokens <= kSelfTokens && tokens * p.K <= kSelfX) {
+    e = launch_gate_up<T, 1, true>(gate_up, p, st);
+  } else {
+    const bool route = p.choice.ids == nullptr;
+    int32_t* ids = reinterpret_cast<int32_t*>(ws + w.ids);
+    float* weights = reinterpret_cast<float*>(ws + w.weights);
+    e = launch_pdl(prepare_kernel<T>, dim3((unsigned)tokens), dim3(kPrepThreads), 0, st, p, route ? ids : nullptr,
+                   weights);
+    if (e != cudaSuccess) return e;
+    if (route) {
+      p.choice.ids = ids;
+      p.choice.weights = weights;
+    }
+    if (tokens <= 4) e = launch_gate_up<T, 1, false>(gate_up, p, st);
+    else if (tokens <= 8) e = launch_gate_up<T, 2, false>(gate_up, p, st);
+    else e = launch_gate_up<T, 4, false>(gate_up, p, st);
+  }
   if (e != cudaSuccess) return e;
-  if (p.choice.T <= 4) return launch_down<T, 1>(p, st);
-  if (p.choice.T <= 8) return launch_down<T, 2>(p, st);
-  return launch_down<T, 4>(p, st);
+  if (tokens <= 4) return launch_down<T, 1>(down, p, st);
+  if (tokens <= 8) return launch_down<T, 2>(down, p, st);
+  return launch_down<T, 4>(down, p, st);
+}
+
+// Maps of `rows` weight rows of `cols` columns for each expert: boxes of `box`
+// rows x 256 columns, and of their scales for the groups of `stage_cols` columns.
+ck_status make_expert_maps(ck::moe::Maps* m, const uint8_t* q, const void* s, const void* z, int64_t E, int64_t rows,
+                           int64_t cols, int G, uint32_t box, int stage_cols) {
+  ck_status r = make_tmap(&m->w, q, (uint64_t)cols / 2, (uint64_t)(E * rows), (uint64_t)cols / 2, 128, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+  if (r != CK_OK) return r;
+  const uint64_t groups = (uint64_t)(E * (cols / G));
+  r = make_tmap(&m->s, s, (uint64_t)rows, groups, (uint64_t)rows * 2, box, (uint32_t)(stage_cols / G),
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_UINT16);
+  if (r != CK_OK) return r;
+  return make_tmap(&m->z, z, (uint64_t)rows, groups, (uint64_t)rows * 2, box, (uint32_t)(stage_cols / G),
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_UINT16);
 }
 
 struct MoeArgs {
@@ -124,18 +183,24 @@ ck_status moe_impl(const char* who, const MoeArgs& a, const ck::moe::Choice& cho
     return fail(CK_ERR_INVALID_ARG, "%s: x, the weights, scales and zeros must be 16-byte aligned", who);
   if (!aligned(a.out, 2)) return fail(CK_ERR_INVALID_ARG, "%s: misaligned output", who);
   if (!aligned(a.ws, 256)) return fail(CK_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
-  const size_t need = ck_moe_awq_w4a16_workspace_bytes(a.T, choice.k, a.I);
-  if (a.ws_bytes < need)
-    return fail(CK_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", who, a.ws_bytes, need);
+  const MoeWorkspace w(a.T, choice.k, a.K, a.I);
+  if (a.ws_bytes < w.total)
+    return fail(CK_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", who, a.ws_bytes, w.total);
   Params p;
   p.choice = choice;
   p.x = a.x; p.ldx = a.ldx; p.K = (int)a.K; p.I = (int)a.I;
   p.gsh = a.G == 64 ? 0 : a.G == 128 ? 1 : 2;
-  p.gate_up_q = a.gq; p.gate_up_s = a.gs; p.gate_up_z = a.gz;
-  p.down_q = a.dq; p.down_s = a.ds; p.down_z = a.dz;
-  p.h = reinterpret_cast<__nv_bfloat16*>(a.ws);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.ws);
+  p.xq = {ws + w.xq, reinterpret_cast<float2*>(ws + w.xs), 2 * a.K, (int)(a.K / 64)};
+  p.hq = {ws + w.hq, reinterpret_cast<float2*>(ws + w.hs), 2 * a.I, (int)(a.I / 64)};
   p.out = a.out;
-  const cudaError_t e = a.dt == CK_BF16 ? launch_moe<__nv_bfloat16>(p, st) : launch_moe<__half>(p, st);
+  Maps gate_up, down;
+  ck_status r = make_expert_maps(&gate_up, a.gq, a.gs, a.gz, a.E, 2 * a.I, a.K, a.G, kColsItem, 256);
+  if (r != CK_OK) return r;
+  r = make_expert_maps(&down, a.dq, a.ds, a.dz, a.E, a.K, a.I, a.G, kRowsTile, 1024);
+  if (r != CK_OK) return r;
+  const cudaError_t e = a.dt == CK_BF16 ? launch_moe<__nv_bfloat16>(gate_up, down, p, ws, w, st)
+                                        : launch_moe<__half>(gate_up, down, p, ws, w, st);
   if (e != cudaSuccess) return fail(CK_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
   return launch_status(who);
 }
@@ -193,8 +258,8 @@ ck_status ck_moe_route(const void* logits, ck_dtype lt, int64_t T, int64_t E, in
   return launch_status(who);
 }
 
-size_t ck_moe_awq_w4a16_workspace_bytes(int64_t T, int top_k, int64_t I) {
-  return T <= 0 || top_k <= 0 || I <= 0 ? 0 : (size_t)T * (size_t)top_k * (size_t)I * 4;   // h as hi, lo
+size_t ck_moe_awq_w4a16_workspace_bytes(int64_t T, int top_k, int64_t K, int64_t I) {
+  return T <= 0 || top_k <= 0 || K <= 0 || I <= 0 ? 0 : MoeWorkspace(T, top_k, K, I).total;
 }
 
 ck_status ck_moe_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_t K, int64_t I, int64_t E, int64_t ldx,

@@ -144,27 +144,30 @@ struct Choice {
 // memory. The slots that some token fills are numbered by (expert, token); a
 // unit is at most `cap` consecutive slots of one expert.
 struct Lists {
-  unsigned long long mask[kMaxExperts];              // tokens of each expert
-  float w[kMaxSlots];                                // the choice as given
-  int16_t id[kMaxSlots];
   float slot_w[kMaxSlots];
-  uint8_t slot_token[kMaxSlots];
   uint16_t unit_expert[kMaxSlots];
   uint16_t unit_start[kMaxSlots];
   uint8_t unit_n[kMaxSlots];
+  uint8_t slot_token[kMaxSlots];
   int warp_sum[32];
   int n_units;
 };
+// What only the building of the lists needs; its memory may be used again afterwards.
+struct ListsTemp {
+  unsigned long long mask[kMaxExperts];              // tokens of each expert
+  float w[kMaxSlots];                                // the choice as given
+  int16_t id[kMaxSlots];
+};
 
-// Fills L from the choice, by all THREADS threads of the CTA (2 THREADS >=
-// kMaxExperts); the lists may be read after the closing barrier. An expert
-// that a token names twice gets it once, with the sum of the two weights. The
-// order is fixed, so every CTA of both kernels builds the same lists.
+// Fills L from the choice, by all THREADS threads of the CTA; the lists may be
+// read, and `tmp` used for something else, after the closing barrier. An
+// expert that a token names twice gets it once, with the sum of the two weights.
+// The order is fixed, so every CTA of both kernels builds the same lists.
 template <int THREADS>
-__device__ __forceinline__ void build_lists(const Choice& c, Lists& L, int cap) {
+__device__ __forceinline__ void build_lists(const Choice& c, Lists& L, ListsTemp& tmp, int cap) {
   static_assert(2 * THREADS >= kMaxExperts, "two experts a thread");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int e = tid; e < c.E; e += THREADS) L.mask[e] = 0ull;
+  for (int e = tid; e < c.E; e += THREADS) tmp.mask[e] = 0ull;
   const int slots = c.T * c.k;
   if (c.ids == nullptr) {
     for (int t = warp; t < c.T; t += THREADS / 32) {
@@ -172,26 +175,26 @@ __device__ __forceinline__ void build_lists(const Choice& c, Lists& L, int cap) 
       float w;
       choose_any(c.logits, c.ldt, t, c.E, c.k, c.renorm != 0, id, w);
       if (lane < c.k) {
-        L.id[t * c.k + lane] = (int16_t)id;
-        L.w[t * c.k + lane] = w;
+        tmp.id[t * c.k + lane] = (int16_t)id;
+        tmp.w[t * c.k + lane] = w;
       }
     }
   } else {
     for (int s = tid; s < slots; s += THREADS) {
       const int id = __ldcg(c.ids + s);
-      L.id[s] = (int16_t)(id >= 0 && id < c.E ? id : -1);
-      L.w[s] = __ldcg(c.weights + s);
+      tmp.id[s] = (int16_t)(id >= 0 && id < c.E ? id : -1);
+      tmp.w[s] = __ldcg(c.weights + s);
     }
   }
   __syncthreads();
   for (int s = tid; s < slots; s += THREADS)
-    if (L.id[s] >= 0) atomicOr(&L.mask[L.id[s]], 1ull << (s / c.k));
+    if (tmp.id[s] >= 0) atomicOr(&tmp.mask[tmp.id[s]], 1ull << (s / c.k));
   __syncthreads();
   int n[2], v = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int e = 2 * tid + i;
-    n[i] = e < c.E ? __popcll(L.mask[e]) : 0;
+    n[i] = e < c.E ? __popcll(tmp.mask[e]) : 0;
     v += ((n[i] + cap - 1) / cap) << 16 | n[i];      // units and slots in one word: both at most kMaxSlots
   }
   int incl = v;
@@ -214,16 +217,17 @@ __device__ __forceinline__ void build_lists(const Choice& c, Lists& L, int cap) 
       L.unit_start[unit] = (uint16_t)(slot + s);
       L.unit_n[unit] = (uint8_t)min(cap, n[i] - s);
     }
-    for (unsigned long long m = L.mask[e]; m != 0ull; m &= m - 1, ++slot) {
+    for (unsigned long long m = tmp.mask[e]; m != 0ull; m &= m - 1, ++slot) {
       const int t = __ffsll((long long)m) - 1;
       float w = 0.0f;
       for (int j = 0; j < c.k; ++j)
-        if (L.id[t * c.k + j] == e) w += L.w[t * c.k + j];
+        if (tmp.id[t * c.k + j] == e) w += tmp.w[t * c.k + j];
       L.slot_token[slot] = (uint8_t)t;
       L.slot_w[slot] = w;
     }
   }
   if (tid == THREADS - 1) L.n_units = (before + incl) >> 16;
+  fence_proxy_async_smem();                          // tmp may become the target of tensor copies
   __syncthreads();
 }
 

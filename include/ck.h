@@ -413,7 +413,7 @@ ck_status ck_moe_route(const void* logits, ck_dtype lt, int64_t T, int64_t E, in
  *             the workspace or other inputs.
  * group_size G : 64, 128 or 256, and a divisor of K and I.
  * x, the weights, scales and zeros are 16-byte aligned; the workspace is
- * 256-byte aligned, at least ck_moe_awq_w4a16_workspace_bytes(T, top_k, I)
+ * 256-byte aligned, at least ck_moe_awq_w4a16_workspace_bytes(T, top_k, K, I)
  * bytes, and belongs to the call until it has run.
  * ck_moe_awq_w4a16 routes by itself, as ck_moe_route does with logits, lt,
  * top_k and renormalize. ck_moe_experts_awq_w4a16 takes the choice: ids and
@@ -423,7 +423,7 @@ ck_status ck_moe_route(const void* logits, ck_dtype lt, int64_t T, int64_t E, in
  * finite gets outputs that are not finite (NaN in general); other tokens are
  * not affected. The result does not depend on timing.
  */
-size_t ck_moe_awq_w4a16_workspace_bytes(int64_t T, int top_k, int64_t I);
+size_t ck_moe_awq_w4a16_workspace_bytes(int64_t T, int top_k, int64_t K, int64_t I);
 ck_status ck_moe_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_t K, int64_t I, int64_t E,
                            int64_t ldx, int group_size, const void* logits, ck_dtype lt, int top_k,
                            int renormalize, const uint8_t* gate_up_q, const void* gate_up_s,

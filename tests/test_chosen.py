@@ -154,7 +154,7 @@ def moe_call(ck, given=False, **kw):
     a = dict(x=p, dt=0, T=4, K=128, I=64, E=8, ldx=128, G=64, logits=p, lt=2, k=2, gq=p, gs=p, gz=p, dq=p, ds=p, dz=p,
              out=p, ws=P(1 << 21), bytes=None, ids=p, w=p)
     a.update(kw)
-    n = ck.moe_awq_w4a16_workspace_bytes(a["T"], a["k"], a["I"]) if a["bytes"] is None else a["bytes"]
+    n = ck.moe_awq_w4a16_workspace_bytes(a["T"], a["k"], a["K"], a["I"]) if a["bytes"] is None else a["bytes"]
     head = (a["x"], a["dt"], a["T"], a["K"], a["I"], a["E"], a["ldx"], a["G"])
     tail = (a["gq"], a["gs"], a["gz"], a["dq"], a["ds"], a["dz"], a["out"], a["ws"], n, None)
     if given:
@@ -187,8 +187,9 @@ def test_moe_choice_validation(ck):
     assert moe_call(ck, True, ids=None) == 1
     assert moe_call(ck, True, w=None) == 1
     assert moe_call(ck, True, w=P((1 << 20) + 2)) == 1
-    assert ck.moe_awq_w4a16_workspace_bytes(4, 2, 64) == 4 * 2 * 64 * 4
-    assert ck.moe_awq_w4a16_workspace_bytes(0, 2, 64) == 0
+    # x and h in two bytes a value and 8 bytes for each 64 of them, the choice: each rounded up to 256 bytes
+    assert ck.moe_awq_w4a16_workspace_bytes(4, 2, 128, 64) == 1024 + 256 + 1024 + 256 + 256 + 256
+    assert ck.moe_awq_w4a16_workspace_bytes(0, 2, 128, 64) == 0
 
 
 def lora_call(ck, **kw):
@@ -403,7 +404,7 @@ def test_moe_strided_x_in_place_and_workspace_bounds(on_gpu):
     x = wide[:, 8:8 + K]
     ref = on_gpu.moe_awq_w4a16(x.contiguous(), logits, k, *gu, *dn)
     assert torch.equal(on_gpu.moe_awq_w4a16(x, logits, k, *gu, *dn), ref)
-    need = on_gpu.moe_awq_w4a16_workspace_bytes(T, k, I)
+    need = on_gpu.moe_awq_w4a16_workspace_bytes(T, k, K, I)
     ws = torch.full((need + 256,), 0xA5, device=DEV, dtype=torch.uint8)
     buf = torch.full((T + 2, K), 7.0, device=DEV, dtype=FP)
     on_gpu.moe_awq_w4a16(x, logits, k, *gu, *dn, workspace=ws[:need], out=buf[1:-1])
@@ -440,7 +441,7 @@ def test_moe_graph_replay_streams_and_a_shared_workspace(on_gpu):
     gu, dn = experts(E, K, I, 64, BF, 13)
     gu, dn = to_dev(gu), to_dev(dn)
     x, logits = torch.randn((T, K), device=DEV).to(BF), torch.randn((T, E), device=DEV)
-    ws = torch.empty(on_gpu.moe_awq_w4a16_workspace_bytes(T, k, I), device=DEV, dtype=torch.uint8)
+    ws = torch.empty(on_gpu.moe_awq_w4a16_workspace_bytes(T, k, K, I), device=DEV, dtype=torch.uint8)
     out, out2 = torch.empty_like(x), torch.empty_like(x)
     side = torch.cuda.Stream()
     graphs = []
