@@ -53,42 +53,56 @@ ck_status check_logits(const char* who, const void* logits, ck_dtype lt) {
 
 // -------------------------------------------------------- mixture of experts
 
-template <typename T, int NT, bool SELF>
-cudaError_t launch_gate_up(const ck::moe::Maps& maps, const ck::moe::Params& p, cudaStream_t st) {
-  using namespace ck::moe;
-  auto kern = gate_up_kernel<T, NT, SELF>;
-  struct Tag {};
-  const int sums = gate_up_sums<NT>() + (SELF ? self_bytes(p.choice.T, p.K) : 0);
-  const int stages = ring_stages(sums, kStreamSmemMax);
-  static_assert(ring_stages(gate_up_sums<NT>() + (SELF ? self_bytes(1, kSelfX) : 0), kStreamSmemMax) >= 2,
-                "two stages at least");
-  const int smem = 1024 + ring_offset(sums) + stages * kStage;
-  const cudaError_t e = set_smem_max<Tag>(kern, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t most = (int64_t)p.choice.T * p.choice.k * (p.I / kColsItem);   // a unit has a slot at least
-  const unsigned grid = (unsigned)std::min<int64_t>(most, 2 * sm_count());
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, maps, p, stages);
+// Stages of `stage` bytes that fit beside what precedes the ring, for `ctas` CTAs on an SM (0: fewer
+// than two do).
+int moe_stages(int offset, int stage, int ctas) {
+  const int room = (228 * 1024) / ctas - 1024;       // 1 KB of an SM's 228 is reserved for each CTA
+  const int n = (std::min(room, 227 * 1024) - 1024 - offset) / stage;   // 1 KB: the base's alignment
+  return n < 2 ? 0 : std::min(n, ck::moe::kMaxStages);
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int KW, bool SELF>
+cudaError_t launch_gate_up(const ck::moe::Maps& maps, const ck::moe::Params& p, cudaStream_t st) {
+  using namespace ck::moe;
+  using C = GateUp<NT, KW, SELF>;
+  auto kern = gate_up_kernel<T, NT, KW, SELF>;
+  struct Tag {};
+  const int offset = ring_offset(p.choice.T * p.choice.k, C::sums(p.choice.T, p.K));
+  int ctas = C::kCtas;
+  while (ctas > 1 && moe_stages(offset, C::kStage, ctas) == 0) --ctas;
+  const int stages = moe_stages(offset, C::kStage, ctas);
+  if (stages == 0) return cudaErrorInvalidValue;
+  const int smem = 1024 + offset + stages * C::kStage;
+  const cudaError_t e = set_smem_max<Tag>(kern, smem, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)p.choice.T * p.choice.k * (p.I / kColsItem);   // a unit has a slot at least
+  const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)ctas * sm_count());
+  return launch_pdl(kern, dim3(grid), dim3(C::kThreads), smem, st, maps, p, stages);
+}
+
+template <typename T, int NT, int SUB>
 cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cudaStream_t st) {
   using namespace ck::moe;
-  auto kern = down_kernel<T, NT>;
+  using C = Down<NT, SUB>;
+  auto kern = down_kernel<T, NT, SUB>;
   struct Tag {};
-  const int sums = down_sums(p.choice.T), stages = ring_stages(sums, kStreamSmemMax);
-  static_assert(ring_stages(down_sums(kMaxTokens), kStreamSmemMax) >= 2, "two stages at least");
-  const int smem = 1024 + ring_offset(sums) + stages * kStage;
-  const cudaError_t e = set_smem_max<Tag>(kern, smem);
+  const int offset = ring_offset(p.choice.T * p.choice.k, C::sums(p.choice.T));
+  int ctas = 3;
+  while (ctas > 1 && moe_stages(offset, C::kStage, ctas) == 0) --ctas;
+  const int stages = moe_stages(offset, C::kStage, ctas);
+  if (stages == 0) return cudaErrorInvalidValue;
+  const int smem = 1024 + offset + stages * C::kStage;
+  const cudaError_t e = set_smem_max<Tag>(kern, smem, 227 * 1024);
   if (e != cudaSuccess) return e;
   const int tiles = p.K / kRowsTile;
   int cs = 8;
-  while (cs > 1 && tiles * cs > 2 * sm_count()) cs /= 2;
-  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kThreads, smem, st, maps, p, stages);
+  while (cs > 1 && tiles * cs > ctas * sm_count()) cs /= 2;
+  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, C::kThreads, smem, st, maps, p, stages);
 }
 
 // Workspace: x as fixed point, h as fixed point, the choice (prepare_kernel's).
 struct MoeWorkspace {
-  size_t xq, xs, hq, hs, ids, weights, total;
+  size_t xq, hq, ids, weights, total;
   MoeWorkspace(int64_t T, int k, int64_t K, int64_t I) {
     size_t at = 0;
     auto take = [&at](int64_t bytes) {
@@ -96,15 +110,21 @@ struct MoeWorkspace {
       at = (at + (size_t)bytes + 255) / 256 * 256;
       return a;
     };
-    xq = take(T * K * 2);
-    xs = take(T * (K / 64) * 8);
-    hq = take(T * k * I * 2);
-    hs = take(T * k * (I / 64) * 8);
+    xq = take(T * ck::moe::row_bytes((int)K));
+    hq = take(T * k * ck::moe::row_bytes((int)I));
     ids = take(T * k * 4);
     weights = take(T * k * 4);
     total = at;
   }
 };
+
+// Which kernels a call runs. One CTA an SM with 16 consumer warps and x converted by each CTA for
+// up to 4 tokens; else three CTAs an SM.
+bool moe_self(const ck::moe::Params& p) {
+  return p.choice.T <= ck::moe::kSelfTokens && p.choice.T * ck::moe::row_bytes(p.K) <= ck::moe::kSelfBytes;
+}
+int gate_up_stage_cols(const ck::moe::Params& p) { return moe_self(p) ? 512 : 256; }
+int down_stage_cols(const ck::moe::Params& p) { return p.choice.T <= 8 ? 512 : 256; }
 
 template <typename T>
 cudaError_t launch_moe(const ck::moe::Maps& gate_up, const ck::moe::Maps& down, ck::moe::Params& p, uint8_t* ws,
@@ -112,8 +132,8 @@ cudaError_t launch_moe(const ck::moe::Maps& gate_up, const ck::moe::Maps& down, 
   using namespace ck::moe;
   const int tokens = p.choice.T;
   cudaError_t e;
-  if (tokens <= kSelfTokens && tokens * p.K <= kSelfX) {
-    e = launch_gate_up<T, 1, true>(gate_up, p, st);
+  if (moe_self(p)) {
+    e = launch_gate_up<T, 1, 4, true>(gate_up, p, st);
   } else {
     const bool route = p.choice.ids == nullptr;
     int32_t* ids = reinterpret_cast<int32_t*>(ws + w.ids);
@@ -125,28 +145,28 @@ cudaError_t launch_moe(const ck::moe::Maps& gate_up, const ck::moe::Maps& down, 
       p.choice.ids = ids;
       p.choice.weights = weights;
     }
-    if (tokens <= 4) e = launch_gate_up<T, 1, false>(gate_up, p, st);
-    else if (tokens <= 8) e = launch_gate_up<T, 2, false>(gate_up, p, st);
-    else e = launch_gate_up<T, 4, false>(gate_up, p, st);
+    if (tokens <= 4) e = launch_gate_up<T, 1, 2, false>(gate_up, p, st);
+    else if (tokens <= 8) e = launch_gate_up<T, 2, 2, false>(gate_up, p, st);
+    else e = launch_gate_up<T, 4, 2, false>(gate_up, p, st);
   }
   if (e != cudaSuccess) return e;
-  if (tokens <= 4) return launch_down<T, 1>(down, p, st);
-  if (tokens <= 8) return launch_down<T, 2>(down, p, st);
-  return launch_down<T, 4>(down, p, st);
+  if (tokens <= 4) return launch_down<T, 1, 2>(down, p, st);
+  if (tokens <= 8) return launch_down<T, 2, 2>(down, p, st);
+  return launch_down<T, 4, 1>(down, p, st);
 }
 
-// Maps of `rows` weight rows of `cols` columns for each expert: boxes of `box`
+// Maps of `rows` weight rows of `cols` columns for each expert: boxes of 64
 // rows x 256 columns, and of their scales for the groups of `stage_cols` columns.
 ck_status make_expert_maps(ck::moe::Maps* m, const uint8_t* q, const void* s, const void* z, int64_t E, int64_t rows,
-                           int64_t cols, int G, uint32_t box, int stage_cols) {
-  ck_status r = make_tmap(&m->w, q, (uint64_t)cols / 2, (uint64_t)(E * rows), (uint64_t)cols / 2, 128, box,
+                           int64_t cols, int G, int stage_cols) {
+  ck_status r = make_tmap(&m->w, q, (uint64_t)cols / 2, (uint64_t)(E * rows), (uint64_t)cols / 2, 128, 64,
                           CU_TENSOR_MAP_SWIZZLE_128B);
   if (r != CK_OK) return r;
   const uint64_t groups = (uint64_t)(E * (cols / G));
-  r = make_tmap(&m->s, s, (uint64_t)rows, groups, (uint64_t)rows * 2, box, (uint32_t)(stage_cols / G),
+  r = make_tmap(&m->s, s, (uint64_t)rows, groups, (uint64_t)rows * 2, 64, (uint32_t)(stage_cols / G),
                 CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_UINT16);
   if (r != CK_OK) return r;
-  return make_tmap(&m->z, z, (uint64_t)rows, groups, (uint64_t)rows * 2, box, (uint32_t)(stage_cols / G),
+  return make_tmap(&m->z, z, (uint64_t)rows, groups, (uint64_t)rows * 2, 64, (uint32_t)(stage_cols / G),
                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_UINT16);
 }
 
@@ -191,13 +211,13 @@ ck_status moe_impl(const char* who, const MoeArgs& a, const ck::moe::Choice& cho
   p.x = a.x; p.ldx = a.ldx; p.K = (int)a.K; p.I = (int)a.I;
   p.gsh = a.G == 64 ? 0 : a.G == 128 ? 1 : 2;
   uint8_t* ws = reinterpret_cast<uint8_t*>(a.ws);
-  p.xq = {ws + w.xq, reinterpret_cast<float2*>(ws + w.xs), 2 * a.K, (int)(a.K / 64)};
-  p.hq = {ws + w.hq, reinterpret_cast<float2*>(ws + w.hs), 2 * a.I, (int)(a.I / 64)};
+  p.xq = ws + w.xq;
+  p.hq = ws + w.hq;
   p.out = a.out;
   Maps gate_up, down;
-  ck_status r = make_expert_maps(&gate_up, a.gq, a.gs, a.gz, a.E, 2 * a.I, a.K, a.G, kColsItem, 256);
+  ck_status r = make_expert_maps(&gate_up, a.gq, a.gs, a.gz, a.E, 2 * a.I, a.K, a.G, gate_up_stage_cols(p));
   if (r != CK_OK) return r;
-  r = make_expert_maps(&down, a.dq, a.ds, a.dz, a.E, a.K, a.I, a.G, kRowsTile, 1024);
+  r = make_expert_maps(&down, a.dq, a.ds, a.dz, a.E, a.K, a.I, a.G, down_stage_cols(p));
   if (r != CK_OK) return r;
   const cudaError_t e = a.dt == CK_BF16 ? launch_moe<__nv_bfloat16>(gate_up, down, p, ws, w, st)
                                         : launch_moe<__half>(gate_up, down, p, ws, w, st);

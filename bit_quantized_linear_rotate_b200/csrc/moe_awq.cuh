@@ -14,7 +14,7 @@
 // Products. Activations enter as 15-bit block fixed point: the 64 columns of a
 // sub-block (which lies in one quantization group, G % 64 == 0) share a scale
 // d = max |x| / 16256, and x ~ d q with q = 128 hi + lo, hi and lo in int8. Then
-//   sum of W x over the sub-block = s d (128 sum u hi + sum u lo) + (z - 8 s) X,  X = d sum q.
+//   sum of W x over the sub-block = s (d (128 sum u hi + sum u lo) - 8 X) + z X,  X = d sum q.
 // The sums are exact int32 products of mma.sync.m16n8k32 (16 weight rows, unsigned
 // nibbles; 8 columns of B: hi and lo of four tokens), below 2^24 and so exact as
 // floats, and the rest is 32-bit floating point. The rounding to 15 bits moves x
@@ -30,6 +30,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "cluster_mem.cuh"
 #include "gemv_awq.cuh"
 #include "moe_route.cuh"
@@ -37,37 +39,24 @@
 namespace ck {
 namespace moe {
 
-constexpr int kCons = 8;               // consumer warps; one more warp feeds the ring
-constexpr int kThreads = 32 * (kCons + 1);
 constexpr int kColsItem = 64;          // columns of h in one item of gate_up_kernel: one block of the fixed point
-constexpr int kRowsTile = 32;          // output columns of one cluster of down_kernel
-constexpr int kMaxStages = 4;
+constexpr int kRowsTile = 64;          // output columns of one cluster of down_kernel
+constexpr int kMaxStages = 6;
 
-// A stage of either ring: 16 KB of weights in boxes of 256 columns (128 bytes a row,
-// 128-byte swizzle), then scales and zeros. In gate_up_kernel 256 columns of 64 gate
-// and 64 up rows, in down_kernel 1024 columns of 32 rows.
-constexpr int kStageW = 128 * 128;
-constexpr int kStageS = 2048;
-constexpr int kStage = kStageW + kStageS;
-
-// Rows of activations as fixed point. Sub-block sb of row r: 128 bytes at q + r *
-// q_stride + 128 sb, the hi bytes of its 64 columns, then the lo bytes, each in
-// four runs of 16 columns in the order 0 2 4 6 1 3 5 7 8 10 12 14 9 11 13 15 (low
-// nibbles of a packed word, then its high nibbles), and {d, X} at scale[r * s_stride + sb].
-struct Fixed {
-  uint8_t* q;
-  float2* scale;
-  int64_t q_stride;                    // bytes: 2 x columns
-  int s_stride;                        // columns / 64
-};
+// Rows of activations as fixed point, in records of four sub-blocks: for each of
+// them 128 bytes, the hi bytes of its 64 columns, then the lo bytes, both in four
+// runs of 16 columns in the order 0 2 4 6 1 3 5 7 8 10 12 14 9 11 13 15 (low nibbles of a packed
+// word, then its high nibbles); behind the four, {d, X} of each.
+constexpr int kRecord = 4 * 128 + 4 * 8;
+__host__ __device__ constexpr int row_bytes(int columns) { return (columns + 255) / 256 * kRecord; }
 
 struct Params {
   Choice choice;
   const void* x;                       // (T, K) T, row stride ldx
   int64_t ldx;
   int K, I, gsh;                       // quantization group of sub-block sb: sb >> gsh
-  Fixed xq;                            // (T) rows by prepare_kernel; unused where a CTA converts x itself
-  Fixed hq;                            // (slots) rows of h
+  uint8_t* xq;                         // (T) rows of x by prepare_kernel; unused where a CTA converts x itself
+  uint8_t* hq;                         // (slots) rows of h
   void* out;                           // (T, K) T
 };
 
@@ -99,7 +88,7 @@ __device__ __forceinline__ int fixed_point(float v, float inv) {
 // Converts row `row` of x (K values) by a group of THREADS threads (a multiple of 8), 8 columns
 // a thread at a time; lane groups of eight hold a sub-block.
 template <typename T, int THREADS>
-__device__ __forceinline__ void convert_row(const T* x, int K, uint8_t* q, float2* scale, int tid) {
+__device__ __forceinline__ void convert_row(const T* x, int K, uint8_t* row, int tid) {
   const int blocks = K >> 6;
   for (int b0 = 0; b0 < blocks; b0 += THREADS / 8) {   // the whole warp stays for the shuffles
     const int sb = b0 + tid / 8, part = tid & 7;
@@ -126,9 +115,11 @@ __device__ __forceinline__ void convert_row(const T* x, int K, uint8_t* q, float
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (in) {
-      *reinterpret_cast<uint2*>(q + sb * 128 + part * 8) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(q + sb * 128 + 64 + part * 8) = make_uint2(lo[0], lo[1]);
-      if (part == 0) scale[sb] = make_float2(d.x, d.x * (float)sum);
+      uint8_t* rec = row + (sb >> 2) * kRecord;
+      uint8_t* q = rec + (sb & 3) * 128 + part * 8;
+      *reinterpret_cast<uint2*>(q) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(q + 64) = make_uint2(lo[0], lo[1]);
+      if (part == 0) reinterpret_cast<float2*>(rec + 512)[sb & 3] = make_float2(d.x, d.x * (float)sum);
     }
   }
 }
@@ -144,8 +135,8 @@ __global__ void __launch_bounds__(kPrepThreads)
   grid_dep_wait();
   grid_dep_launch();
   const int t = blockIdx.x;
-  convert_row<T, kPrepThreads>(reinterpret_cast<const T*>(p.x) + t * p.ldx, p.K, p.xq.q + t * p.xq.q_stride,
-                               p.xq.scale + (int64_t)t * p.xq.s_stride, threadIdx.x);
+  convert_row<T, kPrepThreads>(reinterpret_cast<const T*>(p.x) + t * p.ldx, p.K, p.xq + (int64_t)t * row_bytes(p.K),
+                               threadIdx.x);
   if (ids != nullptr && threadIdx.x < 32) {
     int id;
     float w;
@@ -192,21 +183,18 @@ __device__ __forceinline__ void mma_u8s8(int (&c)[4], const uint32_t (&a)[4], ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// tot += the sub-block's sum of W x, for the tile's rows r and r + 1 and token t of the four in b.
-// s, z8: the rows' scales and z - 8 s; dx: {d, X} of that token's block.
+// tot += the sub-block's sum of W x = s (d I - 8 X) + z X, for the tile's rows r and r + 1 and
+// token t of the four in b. dx: {d, X} of that token's block.
 __device__ __forceinline__ void add_block(float (&tot)[2], const uint32_t (&a)[2][4], const uint4 b, const float2 s,
-                                          const float2 z8, const float2 dx) {
+                                          const float2 z, const float2 dx) {
   int c[4] = {0, 0, 0, 0};
   mma_u8s8(c, a[0], b.x, b.y);
   mma_u8s8(c, a[1], b.z, b.w);
-  tot[0] += (s.x * dx.x) * (float)(c[0] * 128 + c[1]);
-  tot[1] += (s.y * dx.x) * (float)(c[2] * 128 + c[3]);
-  tot[0] = fmaf(z8.x, dx.y, tot[0]);
-  tot[1] = fmaf(z8.y, dx.y, tot[1]);
-}
-
-__device__ __forceinline__ float2 fold_zero(const float2 s, const float2 z) {
-  return make_float2(fmaf(-8.0f, s.x, z.x), fmaf(-8.0f, s.y, z.y));
+  const float x8 = -8.0f * dx.y;
+  tot[0] = fmaf(s.x, fmaf(dx.x, (float)(c[0] * 128 + c[1]), x8), tot[0]);
+  tot[1] = fmaf(s.y, fmaf(dx.x, (float)(c[2] * 128 + c[3]), x8), tot[1]);
+  tot[0] = fmaf(z.x, dx.y, tot[0]);
+  tot[1] = fmaf(z.y, dx.y, tot[1]);
 }
 
 // ------------------------------------------------------------------ the ring
@@ -220,200 +208,240 @@ struct Ring {
   int abort;
 };
 
-__device__ __forceinline__ void ring_init(Ring& R, int stages) {
+__device__ __forceinline__ void ring_init(Ring& R, int stages, int consumers) {
   for (int s = 0; s < stages; ++s) {
     mbar_init(&R.full[s], 1);
-    mbar_init(&R.empty[s], kCons);
+    mbar_init(&R.empty[s], consumers);
   }
   R.abort = 0;
   fence_mbarrier_init();
 }
 
-// Producer (one thread): waits until fill i may overwrite its stage.
-__device__ __forceinline__ bool ring_claim(Ring& R, int stages, int i) {
-  return i < stages || mbar_wait(&R.empty[i % stages], (i / stages - 1) & 1, &R.abort, 50);
+// Where a thread is in the ring: its stage, and the parity of that stage's round.
+struct Cursor {
+  int stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) stage = 0, parity ^= 1;
+  }
+};
+
+// Producer (one thread): waits until the stage may be overwritten (at once in the first round).
+__device__ __forceinline__ bool ring_claim(Ring& R, const Cursor& c) {
+  return mbar_wait(&R.empty[c.stage], c.parity ^ 1, &R.abort, 50);
 }
 
-// Producer: after giving up, waits (with a limit) for the copies in flight.
-__device__ __forceinline__ void ring_drain(Ring& R, int stages, int issued) {
-  for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
-    mbar_wait(&R.full[i % stages], (i / stages) & 1, nullptr, 51, 100000000ull);
+// Producer: after giving up, waits (with a limit) for the copies in flight: every stage's last fill.
+__device__ __forceinline__ void ring_drain(Ring& R, Cursor c, int stages, int issued) {
+  for (int i = 0; i < issued && i < stages; ++i) {
+    if (c.stage == 0) c.stage = stages, c.parity ^= 1;
+    --c.stage;
+    mbar_wait(&R.full[c.stage], c.parity, nullptr, 51, 100000000ull);
+  }
 }
 
-__device__ __forceinline__ void ring_await(Ring& R, int stages, int i) {
-  warp_wait(&R.full[i % stages], (i / stages) & 1, &R.abort, 52);
+__device__ __forceinline__ void ring_await(Ring& R, const Cursor& c) {
+  warp_wait(&R.full[c.stage], c.parity, &R.abort, 52);
 }
 
-__device__ __forceinline__ void ring_release(Ring& R, int stages, int i) {
+__device__ __forceinline__ void ring_release(Ring& R, const Cursor& c) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&R.empty[i % stages]);
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&R.empty[c.stage]);
 }
 
 // The consumer warps' own barrier.
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kCons) : "memory"); }
-
-// Shared memory: the lists, what each kernel sums in, and the ring, whose memory the
-// building of the lists uses first.
-struct SmemHead {
-  Lists L;
-  Ring R;
-};
-constexpr int kHead = (sizeof(SmemHead) + 127) / 128 * 128;
-static_assert(sizeof(ListsTemp) <= kStage, "the lists are built in the ring's first stage");
-
-// Offset of the ring behind `sums` bytes: 1024-byte aligned boxes.
-__host__ __device__ constexpr int ring_offset(int sums) { return (kHead + sums + 1023) / 1024 * 1024; }
-
-// Up to kMaxStages stages that leave room for two CTAs on an SM (max_smem each, with
-// 1024 bytes for aligning the base).
-__host__ __device__ constexpr int ring_stages(int sums, int max_smem) {
-  const int n = (max_smem - 1024 - ring_offset(sums)) / kStage;
-  return n < kMaxStages ? n : kMaxStages;
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
+
+// Global memory that earlier kernels wrote may be read by bulk copies from here on.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// Shared memory of both kernels: the ring's barriers, the lists, what the kernel sums in, and
+// the ring (1024-byte aligned stages), whose memory the building of the lists uses first.
+constexpr int kHead = (sizeof(Ring) + 127) / 128 * 128;
+__host__ __device__ constexpr int ring_offset(int slots, int sums) {
+  return (kHead + (lists_bytes(slots) + 127) / 128 * 128 + sums + 1023) / 1024 * 1024;
+}
+
+__device__ __forceinline__ uint8_t* align_1024(uint8_t* p) { return p + ((1024 - (smem_u32(p) & 1023)) & 1023); }
 
 // -------------------------------------------------------------- gate and up
 
 // An item is 64 columns of h of one unit (an expert's tokens, at most 4 NT): 64
 // gate rows and the 64 up rows that belong to them. A CTA takes a contiguous
-// share of the items and streams their weights, 256 columns a stage. Consumer
-// warp (kw, hf) multiplies 32 gate and 32 up rows with sub-block kw of each stage; the
-// four partial sums meet in shared memory, where one warp a token forms h and
-// converts it to fixed point.
+// share of the items and streams their weights, with the unit's rows of x, 128 KW
+// columns a stage. Consumer warp (kw, rq) multiplies 16 gate and 16 up rows with sub-blocks kw
+// and kw + KW of each stage; the KW partial sums meet in shared memory, where
+// one warp a token forms h and converts it to fixed point.
 //
-// SELF: x is converted by every CTA, into shared memory (T <= 4 and T K <=
-// kSelfX): the launch of prepare_kernel and the wait for it cost more.
-constexpr int kSelfTokens = 4, kSelfX = 16384;
+// SELF: every CTA converts x itself, into shared memory (T <= kSelfTokens): the launch of
+// prepare_kernel and the wait for it cost more.
+constexpr int kSelfTokens = 4, kSelfBytes = 64 * 1024;
 
-template <int NT>
-__host__ __device__ constexpr int gate_up_sums() { return 4 * 2 * 4 * NT * 32 * 8; }   // float2 [kw][hf][tile][token tile][lane]
+template <int NT, int KW, bool SELF>
+struct GateUp {
+  static constexpr int kCons = 4 * KW, kThreads = 32 * (kCons + 1);
+  static constexpr int kCtas = KW == 2 ? 3 : 1;                 // on an SM
+  static constexpr int kSubs = 2 * KW;                          // sub-blocks a stage
+  static constexpr int kW = kSubs * 64 * 32;                    // its bytes of gate (or up) weights
+  static constexpr int kS = kSubs * 128;                        // bytes of each kind of scales
+  static constexpr int kRows = SELF ? 0 : 4 * NT * (kSubs / 4) * kRecord;
+  static constexpr int kStage = (2 * kW + 4 * kS + kRows + 1023) / 1024 * 1024;
+  static constexpr int kRed = KW * 4 * 2 * NT * 32 * 8;         // float2 [kw][rq][gate, up][token tile][lane]
+  __host__ __device__ static constexpr int sums(int T, int K) { return kRed + (SELF ? T * row_bytes(K) : 0); }
+};
 
-// Bytes of T rows of fixed point in shared memory.
-__host__ __device__ constexpr int self_bytes(int T, int K) { return T * (2 * K + (K >> 6) * 8); }
-
-template <typename T, int NT, bool SELF>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int NT, int KW, bool SELF>
+__global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW, SELF>::kCtas)
     gate_up_kernel(const __grid_constant__ Maps maps, const Params p, int stages) {
+  using C = GateUp<NT, KW, SELF>;
   extern __shared__ uint8_t sm_raw[];
-  uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  SmemHead& S = *reinterpret_cast<SmemHead*>(sm);
-  float2* red = reinterpret_cast<float2*>(sm + kHead);
-  const int tokens = p.choice.T;
-  uint8_t* own = sm + kHead + gate_up_sums<NT>();
-  uint8_t* ring = sm + ring_offset(gate_up_sums<NT>() + (SELF ? self_bytes(tokens, p.K) : 0));
+  uint8_t* sm = align_1024(sm_raw);
+  Ring& R = *reinterpret_cast<Ring*>(sm);
+  const int tokens = p.choice.T, slots = tokens * p.choice.k;
+  const Lists L = lists_at(sm + kHead, slots);
+  float2* red = reinterpret_cast<float2*>(sm + kHead + (lists_bytes(slots) + 127) / 128 * 128);
+  uint8_t* own = reinterpret_cast<uint8_t*>(red) + C::kRed;
+  uint8_t* ring = sm + ring_offset(slots, C::sums(tokens, p.K));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  if (tid == kThreads - 32) {
+  if (tid == C::kThreads - 32) {
     prefetch_tmap(&maps.w);
     prefetch_tmap(&maps.s);
     prefetch_tmap(&maps.z);
-    ring_init(S.R, stages);
+    ring_init(R, stages, C::kCons);
   }
   grid_dep_wait();
   grid_dep_launch();   // after the wait: the next kernel may read the choice before its own wait
-  build_lists<kThreads>(p.choice, S.L, *reinterpret_cast<ListsTemp*>(ring), 4 * NT);
+  static_assert(sizeof(ListsTemp) <= 2 * C::kStage, "the lists are built in the ring's memory");
+  build_lists<C::kThreads>(p.choice, L, *reinterpret_cast<ListsTemp*>(ring), 4 * NT);
 
-  const int per_unit = p.I / kColsItem, nsub = p.K >> 6, nchunk = (nsub + 3) >> 2;
-  const int64_t items = (int64_t)S.L.n_units * per_unit;
+  const int per_unit = p.I / kColsItem, nsub = p.K >> 6, nchunk = (nsub + C::kSubs - 1) / C::kSubs;
+  const int64_t items = (int64_t)L.units() * per_unit;
   const int i0 = (int)(items * blockIdx.x / gridDim.x), i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
-  const int srows = 4 >> p.gsh;        // rows of scales a stage: its 256 columns' groups
+  const int srows = C::kSubs >> p.gsh;   // rows of scales a stage: its columns' groups
+  const int xrow = row_bytes(p.K);
 
-  if (warp == kCons) {
-    if (lane == 0) {
-      const int ngrp = nsub >> p.gsh;
-      int f = 0;
-      for (int item = i0; item < i1; ++item) {
-        const int u = item / per_unit, c0 = (item % per_unit) * kColsItem;
-        const int e = S.L.unit_expert[u];
-        for (int ch = 0; ch < nchunk; ++ch, ++f) {
-          if (!ring_claim(S.R, stages, f)) break;
-          uint8_t* st = ring + (f % stages) * kStage;
-          uint64_t* bar = &S.R.full[f % stages];
-          mbar_arrive_expect_tx(bar, kStageW + 4 * 128 * srows);
-          tma_load_2d(st, &maps.w, bar, 128 * ch, e * 2 * p.I + c0);
-          tma_load_2d(st + kStageW / 2, &maps.w, bar, 128 * ch, e * 2 * p.I + p.I + c0);
+  if (warp == C::kCons) {
+    fence_proxy_async_all();
+    const int ngrp = nsub >> p.gsh;
+    Cursor at;
+    int issued = 0;
+    bool live = true;
+    for (int item = i0; item < i1 && live; ++item) {
+      const int u = item / per_unit, c0 = (item % per_unit) * kColsItem;
+      const int e = L.unit_expert[u], row = e * 2 * p.I + c0, n = L.unit_n[u];
+      const uint8_t* xr = nullptr;
+      if (!SELF && lane < n) xr = p.xq + (int64_t)L.slot_token[L.unit_start[u] + lane] * xrow;
+      for (int ch = 0; ch < nchunk; ++ch, at.next(stages)) {
+        live = __all_sync(0xffffffffu, ring_claim(R, at));
+        if (!live) break;
+        ++issued;
+        uint8_t* st = ring + at.stage * C::kStage;
+        uint64_t* bar = &R.full[at.stage];
+        const int boxes = min(C::kSubs / 4, (nsub - C::kSubs * ch + 3) >> 2);   // of 256 columns
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, boxes * (2 * 64 * 128 + (SELF ? 0 : n * kRecord)) + 4 * 128 * srows);
+          for (int i = 0; i < boxes; ++i) {
+            tma_load_2d(st + i * 64 * 128, &maps.w, bar, (C::kSubs * ch + 4 * i) * 32, row);
+            tma_load_2d(st + C::kW + i * 64 * 128, &maps.w, bar, (C::kSubs * ch + 4 * i) * 32, row + p.I);
+          }
           const int sr = e * ngrp + ch * srows;
-          tma_load_2d(st + kStageW, &maps.s, bar, c0, sr);
-          tma_load_2d(st + kStageW + 512, &maps.z, bar, c0, sr);
-          tma_load_2d(st + kStageW + 1024, &maps.s, bar, p.I + c0, sr);
-          tma_load_2d(st + kStageW + 1536, &maps.z, bar, p.I + c0, sr);
+          uint8_t* sc = st + 2 * C::kW;
+          tma_load_2d(sc, &maps.s, bar, c0, sr);
+          tma_load_2d(sc + C::kS, &maps.z, bar, c0, sr);
+          tma_load_2d(sc + 2 * C::kS, &maps.s, bar, p.I + c0, sr);
+          tma_load_2d(sc + 3 * C::kS, &maps.z, bar, p.I + c0, sr);
         }
-        if (S.R.abort) break;
+        __syncwarp();
+        if (!SELF && lane < n)
+          bulk_load(st + 2 * C::kW + 4 * C::kS + lane * (C::kSubs / 4) * kRecord, xr + ch * (C::kSubs / 4) * kRecord,
+                    boxes * kRecord, bar);
       }
-      if (S.R.abort) ring_drain(S.R, stages, f);
     }
+    if (!live && lane == 0) ring_drain(R, at, stages, issued);
     return;
   }
 
-  Fixed xq = p.xq;
   if constexpr (SELF) {
-    xq.q = own;
-    xq.q_stride = 2 * p.K;
-    xq.s_stride = nsub;
-    xq.scale = reinterpret_cast<float2*>(own + tokens * 2 * p.K);
     for (int i = 0; i < tokens; ++i)
-      convert_row<T, 32 * kCons>(reinterpret_cast<const T*>(p.x) + i * p.ldx, p.K, xq.q + i * xq.q_stride,
-                                 xq.scale + i * xq.s_stride, tid);
-    consumers_sync();
+      convert_row<T, 32 * C::kCons>(reinterpret_cast<const T*>(p.x) + i * p.ldx, p.K, own + i * xrow, tid);
+    consumers_sync<32 * C::kCons>();
   }
 
-  const int kw = warp >> 1, hf = warp & 1;
-  int f = 0;
+  const int kw = warp >> 2, rq = warp & 3;
+  Cursor at;
+  float tot[2][NT][2];
+  // One item's products with N token tiles; sums in tot.
+  auto products = [&](auto tiles, int start, int n) {
+    constexpr int N = decltype(tiles)::value;
+    // the lane's column of B (hi or lo of token g / 2) and the scales of token t; past the last
+    // token its copies, whose results nobody reads
+    int bq[N], bs[N];
+#pragma unroll
+    for (int tt = 0; tt < N; ++tt) {
+      const int c = min(4 * tt + (g >> 1), n - 1), d = min(4 * tt + t, n - 1);
+      const int rows = SELF ? xrow : (C::kSubs / 4) * kRecord;
+      bq[tt] = (SELF ? L.slot_token[start + c] : c) * rows + (g & 1) * 64 + t * 16;
+      bs[tt] = (SELF ? L.slot_token[start + d] : d) * rows + 512;
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int tt = 0; tt < N; ++tt) tot[m][tt][0] = tot[m][tt][1] = 0.0f;
+    const int r = 16 * rq + 2 * g;
+    for (int ch = 0; ch < nchunk; ++ch, at.next(stages)) {
+      const uint8_t* st = ring + at.stage * C::kStage;
+      const uint8_t* rec = SELF ? own + ch * (C::kSubs / 4) * kRecord : st + 2 * C::kW + 4 * C::kS;
+      ring_await(R, at);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int sb = kw + KW * i;      // of the stage
+        if (C::kSubs * ch + sb >= nsub) break;
+        uint4 b[N];
+        float2 dx[N];
+#pragma unroll
+        for (int tt = 0; tt < N; ++tt) {
+          b[tt] = *reinterpret_cast<const uint4*>(rec + bq[tt] + (sb >> 2) * kRecord + (sb & 3) * 128);
+          dx[tt] = *reinterpret_cast<const float2*>(rec + bs[tt] + (sb >> 2) * kRecord + (sb & 3) * 8);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {    // gate, up
+          uint32_t a[2][4];
+          load_tile(st + m * C::kW + (sb >> 2) * 64 * 128, r, sb, t, a);
+          const uint8_t* sp = st + 2 * C::kW + 2 * m * C::kS + (sb >> p.gsh) * 128 + 2 * r;
+          const float2 s = load_pair<T>(sp), z = load_pair<T>(sp + C::kS);
+#pragma unroll
+          for (int tt = 0; tt < N; ++tt) add_block(tot[m][tt], a, b[tt], s, z, dx[tt]);
+        }
+      }
+      ring_release(R, at);
+    }
+  };
+
   for (int item = i0; item < i1; ++item) {
     const int u = item / per_unit, cb = item % per_unit;
-    const int start = S.L.unit_start[u], n = S.L.unit_n[u];
-    const uint8_t* bq[NT];             // the lane's column of B: hi or lo of token g / 2
-    const float2* bs[NT];              // scales of token t
+    const int start = L.unit_start[u], n = L.unit_n[u], nt = (n + 3) >> 2;
+    if (NT == 1 || n <= 4) products(std::integral_constant<int, 1>(), start, n);
+    else if (NT == 2 || n <= 8) products(std::integral_constant<int, NT < 2 ? 1 : 2>(), start, n);
+    else products(std::integral_constant<int, NT>(), start, n);
+    if (item != i0) consumers_sync<32 * C::kCons>();   // the previous item's sums have been read
 #pragma unroll
-    for (int tt = 0; tt < NT; ++tt) {
-      const int c = min(4 * tt + (g >> 1), n - 1), d = min(4 * tt + t, n - 1);   // past the last: its copies, unused
-      bq[tt] = xq.q + S.L.slot_token[start + c] * xq.q_stride + kw * 128 + (g & 1) * 64 + t * 16;
-      bs[tt] = xq.scale + (int64_t)S.L.slot_token[start + d] * xq.s_stride + kw;
-    }
-    float tot[4][NT][2] = {};
-    for (int ch = 0; ch < nchunk; ++ch, ++f) {
-      const uint8_t* st = ring + (f % stages) * kStage;
-      const bool in = 4 * ch + kw < nsub;
-      uint4 b[NT];
-      float2 dx[NT];
-      if (in) {
-#pragma unroll
-        for (int tt = 0; tt < NT; ++tt) {
-          if (4 * tt >= n) break;
-          b[tt] = *reinterpret_cast<const uint4*>(bq[tt] + ch * 512);
-          dx[tt] = bs[tt][4 * ch];
-        }
-      }
-      ring_await(S.R, stages, f);
-      if (in) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {   // two gate tiles, two up tiles
-          const int r = 32 * hf + 16 * (m & 1) + 2 * g;
-          uint32_t a[2][4];
-          load_tile(st + (m >> 1) * (kStageW / 2), r, kw, t, a);
-          const uint8_t* sp = st + kStageW + (m >> 1) * 1024 + (kw >> p.gsh) * 128 + 2 * r;
-          const float2 s = load_pair<T>(sp), z8 = fold_zero(s, load_pair<T>(sp + 512));
-#pragma unroll
-          for (int tt = 0; tt < NT; ++tt) {
-            if (4 * tt >= n) break;
-            add_block(tot[m][tt], a, b[tt], s, z8, dx[tt]);
-          }
-        }
-      }
-      ring_release(S.R, stages, f);
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int tt = 0; tt < NT; ++tt)
-        red[((warp * 4 + m) * NT + tt) * 32 + lane] = make_float2(tot[m][tt][0], tot[m][tt][1]);
-    consumers_sync();
-    for (int c = warp; c < n; c += kCons) {   // token c of the unit: a lane forms columns 2 lane and 2 lane + 1
-      const int m = (lane >> 3) & 1, ln = (lane & 7) * 4 + (c & 3);
+        if (tt < nt) red[((warp * 2 + m) * NT + tt) * 32 + lane] = make_float2(tot[m][tt][0], tot[m][tt][1]);
+    consumers_sync<32 * C::kCons>();
+    // Token c of the unit: a lane forms columns 2 lane and 2 lane + 1. The other warps go on.
+    for (int c = (warp + item) & (C::kCons - 1); c < n; c += C::kCons) {
+      const int ln = (lane & 7) * 4 + (c & 3);
       float2 gate = make_float2(0.0f, 0.0f), up = gate;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2* q = red + (((2 * w + (lane >> 4)) * 4 + m) * NT + (c >> 2)) * 32 + ln;
-        const float2 a = q[0], b = q[2 * NT * 32];
+      for (int w = 0; w < KW; ++w) {
+        const float2* q = red + (((w * 4 + (lane >> 3)) * 2) * NT + (c >> 2)) * 32 + ln;
+        const float2 a = q[0], b = q[NT * 32];
         gate.x += a.x, gate.y += a.y, up.x += b.x, up.y += b.y;
       }
       const float h0 = gate.x / (1.0f + expf(-gate.x)) * up.x, h1 = gate.y / (1.0f + expf(-gate.y)) * up.y;
@@ -423,149 +451,187 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int a0 = (f0 + 64) >> 7, a1 = (f1 + 64) >> 7;
       const int sum = __reduce_add_sync(0xffffffffu, f0 + f1);
       // columns 8 i + 2 j and + 1 (i = lane / 4, j = lane % 4): byte j of the run's even and odd words
-      uint8_t* q = p.hq.q + (start + c) * p.hq.q_stride + cb * 128 + (lane >> 2) * 8 + (lane & 3);
+      uint8_t* rec = p.hq + (int64_t)(start + c) * row_bytes(p.I) + (cb >> 2) * kRecord;
+      uint8_t* q = rec + (cb & 3) * 128 + (lane >> 2) * 8 + (lane & 3);
       q[0] = (uint8_t)a0;
       q[4] = (uint8_t)a1;
       q[64] = (uint8_t)(f0 - 128 * a0);
       q[68] = (uint8_t)(f1 - 128 * a1);
-      if (lane == 0) p.hq.scale[(int64_t)(start + c) * p.hq.s_stride + cb] = make_float2(d.x, d.x * (float)sum);
+      if (lane == 0) {                   // with the token's weight: down_kernel only adds
+        const float w = L.slot_w[start + c];
+        reinterpret_cast<float2*>(rec + 512)[cb & 3] = make_float2(w * d.x, w * (d.x * (float)sum));
+      }
     }
-    consumers_sync();                   // red is free again
   }
 }
 
 // --------------------------------------------------------------------- down
 
-// A cluster of CTAs owns 32 output columns and walks (unit, 1024 columns of h)
-// steps, each CTA a contiguous share of them; consumer warp w takes sub-blocks w
-// and w + 8 of a step. When the unit changes, each warp adds its sums, times the
-// tokens' weights, to its own (T, 32) accumulator in shared memory; at the end
-// the warps' accumulators and then the CTAs' are added in order. The weights' ring
-// starts before the dependency wait.
-__host__ __device__ constexpr int down_sums(int T) { return kCons * T * kRowsTile * 4; }
+// A cluster of CTAs owns 64 output columns and walks (unit, 256 SUB columns of h)
+// steps, each CTA a contiguous share of them; consumer warp (kw, rh) takes sub-blocks
+// kw (and kw + 4) of a step and 32 of the output columns. When the unit changes, each warp
+// adds its sums to the accumulator (T, 64) that it shares with the other rh; at the
+// end the four accumulators and then the CTAs' are added in order. The weights of
+// the first stages are fetched before the dependency wait, the rows of h after it.
+template <int NT, int SUB>
+struct Down {
+  static constexpr int kCons = 8, kThreads = 32 * (kCons + 1);
+  static constexpr int kSubs = 4 * SUB;
+  static constexpr int kW = kSubs * 64 * 32;
+  static constexpr int kS = kSubs * 128;
+  static constexpr int kStage = (kW + 2 * kS + 4 * NT * SUB * kRecord + 1023) / 1024 * 1024;
+  __host__ __device__ static constexpr int sums(int T) { return 4 * T * kRowsTile * 4; }
+};
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int NT, int SUB>
+__global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
     down_kernel(const __grid_constant__ Maps maps, const Params p, int stages) {
+  using C = Down<NT, SUB>;
   extern __shared__ uint8_t sm_raw[];
-  uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  SmemHead& S = *reinterpret_cast<SmemHead*>(sm);
-  const int tokens = p.choice.T;
-  float* sums = reinterpret_cast<float*>(sm + kHead);
-  uint8_t* ring = sm + ring_offset(down_sums(tokens));
+  uint8_t* sm = align_1024(sm_raw);
+  Ring& R = *reinterpret_cast<Ring*>(sm);
+  const int tokens = p.choice.T, slots = tokens * p.choice.k;
+  const Lists L = lists_at(sm + kHead, slots);
+  float* sums = reinterpret_cast<float*>(sm + kHead + (lists_bytes(slots) + 127) / 128 * 128);
+  uint8_t* ring = sm + ring_offset(slots, C::sums(tokens));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t rank = cluster_ctarank(), ranks = cluster_nctarank();
   const int n0 = (int)(blockIdx.x / ranks) * kRowsTile, cells = tokens * kRowsTile;
-  if (tid == kThreads - 32) {
+  if (tid == C::kThreads - 32) {
     prefetch_tmap(&maps.w);
     prefetch_tmap(&maps.s);
     prefetch_tmap(&maps.z);
-    ring_init(S.R, stages);
+    ring_init(R, stages, C::kCons);
   }
-  for (int i = tid; i < kCons * cells; i += kThreads) sums[i] = 0.0f;
+  for (int i = tid; i < 4 * cells; i += C::kThreads) sums[i] = 0.0f;
   // The choice was complete before gate_up_kernel let this kernel start.
-  build_lists<kThreads>(p.choice, S.L, *reinterpret_cast<ListsTemp*>(ring), 4 * NT);
+  static_assert(sizeof(ListsTemp) <= 2 * C::kStage, "the lists are built in the ring's memory");
+  build_lists<C::kThreads>(p.choice, L, *reinterpret_cast<ListsTemp*>(ring), 4 * NT);
 
-  const int nsub = p.I >> 6, nchunk = (nsub + 15) >> 4;
-  const int64_t steps = (int64_t)S.L.n_units * nchunk;
+  const int nsub = p.I >> 6, nchunk = (nsub + C::kSubs - 1) / C::kSubs;
+  const int64_t steps = (int64_t)L.units() * nchunk;
   const int s0 = (int)(steps * rank / ranks), s1 = (int)(steps * (rank + 1) / ranks);
-  const int srows = 16 >> p.gsh;
+  const int srows = C::kSubs >> p.gsh;
+  const int hrow = row_bytes(p.I);
 
-  if (warp == kCons) {
-    if (lane == 0) {
-      const int ngrp = nsub >> p.gsh;
-      int f = 0;
-      for (int s = s0; s < s1; ++s, ++f) {
-        if (!ring_claim(S.R, stages, f)) break;
-        const int e = S.L.unit_expert[s / nchunk], ch = s % nchunk;
-        uint8_t* st = ring + (f % stages) * kStage;
-        uint64_t* bar = &S.R.full[f % stages];
-        const int boxes = min(4, (nsub - 16 * ch + 3) >> 2);          // of 256 columns
-        mbar_arrive_expect_tx(bar, boxes * (kStageW / 4) + 2 * 64 * srows);
-        for (int i = 0; i < boxes; ++i)
-          tma_load_2d(st + i * (kStageW / 4), &maps.w, bar, 512 * ch + 128 * i, e * p.K + n0);
-        tma_load_2d(st + kStageW, &maps.s, bar, n0, e * ngrp + ch * srows);
-        tma_load_2d(st + kStageW + 1024, &maps.z, bar, n0, e * ngrp + ch * srows);
-      }
-      if (S.R.abort) ring_drain(S.R, stages, f);
-    }
+  if (warp == C::kCons) {
+    const int ngrp = nsub >> p.gsh;
+    // Weights and scales of step s, and the bytes of its rows of h announced.
+    auto fetch_weights = [&](int s, const Cursor& at) {
+      const int u = s / nchunk, ch = s - u * nchunk, e = L.unit_expert[u];
+      uint8_t* st = ring + at.stage * C::kStage;
+      uint64_t* bar = &R.full[at.stage];
+      const int boxes = min(SUB, (nsub - C::kSubs * ch + 3) >> 2);
+      mbar_arrive_expect_tx(bar, boxes * (64 * 128 + L.unit_n[u] * kRecord) + 2 * 128 * srows);
+      for (int i = 0; i < boxes; ++i)
+        tma_load_2d(st + i * 64 * 128, &maps.w, bar, (C::kSubs * ch + 4 * i) * 32, e * p.K + n0);
+      tma_load_2d(st + C::kW, &maps.s, bar, n0, e * ngrp + ch * srows);
+      tma_load_2d(st + C::kW + C::kS, &maps.z, bar, n0, e * ngrp + ch * srows);
+    };
+    auto fetch_rows = [&](int s, const Cursor& at) {
+      const int u = s / nchunk, ch = s - u * nchunk;
+      const int boxes = min(SUB, (nsub - C::kSubs * ch + 3) >> 2);
+      if (lane < L.unit_n[u])
+        bulk_load(ring + at.stage * C::kStage + C::kW + 2 * C::kS + lane * SUB * kRecord,
+                  p.hq + (int64_t)(L.unit_start[u] + lane) * hrow + ch * SUB * kRecord, boxes * kRecord,
+                  &R.full[at.stage]);
+    };
+    const int ahead = min(stages, s1 - s0);
+    Cursor at;
+    if (lane == 0)
+      for (int i = 0; i < ahead; ++i, at.next(stages)) fetch_weights(s0 + i, at);
     __syncwarp();
     grid_dep_wait();
     grid_dep_launch();
+    fence_proxy_async_all();
+    at = Cursor();
+    for (int i = 0; i < ahead; ++i, at.next(stages)) fetch_rows(s0 + i, at);
+    int issued = ahead;
+    bool live = true;
+    for (int s = s0 + ahead; s < s1; ++s, ++issued, at.next(stages)) {
+      live = __all_sync(0xffffffffu, ring_claim(R, at));
+      if (!live) break;
+      if (lane == 0) fetch_weights(s, at);
+      __syncwarp();
+      fetch_rows(s, at);
+    }
+    if (!live && lane == 0) ring_drain(R, at, stages, issued);
   } else {
     grid_dep_wait();
     grid_dep_launch();
-    float* acc = sums + warp * cells;
-    float tot[2][NT][2] = {};
-    for (int s = s0, f = 0; s < s1; ++s, ++f) {
-      const int u = s / nchunk, ch = s % nchunk;
-      const int start = S.L.unit_start[u], n = S.L.unit_n[u];
-      const uint8_t* st = ring + (f % stages) * kStage;
-      uint4 b[2][NT];
-      float2 dx[2][NT];
+    const int kw = warp >> 1, rh = warp & 1;
+    float* acc = sums + kw * cells + 32 * rh + 2 * g;
+    Cursor at;
+    // `chunks` steps of unit u from chunk ch on, with N token tiles.
+    auto products = [&](auto tiles, int u, int ch, int chunks) {
+      constexpr int N = decltype(tiles)::value;
+      const int start = L.unit_start[u], n = L.unit_n[u];
+      int bq[N], bs[N];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int sb = 16 * ch + warp + 8 * i;
-        if (sb >= nsub) break;
-#pragma unroll
-        for (int tt = 0; tt < NT; ++tt) {
-          if (4 * tt >= n) break;
-          const int c = start + min(4 * tt + (g >> 1), n - 1), d = start + min(4 * tt + t, n - 1);
-          b[i][tt] = *reinterpret_cast<const uint4*>(p.hq.q + c * p.hq.q_stride + sb * 128 + (g & 1) * 64 + t * 16);
-          dx[i][tt] = p.hq.scale[(int64_t)d * p.hq.s_stride + sb];
-        }
+      for (int tt = 0; tt < N; ++tt) {
+        bq[tt] = min(4 * tt + (g >> 1), n - 1) * SUB * kRecord + kw * 128 + (g & 1) * 64 + t * 16;
+        bs[tt] = min(4 * tt + t, n - 1) * SUB * kRecord + 512 + kw * 8;
       }
-      ring_await(S.R, stages, f);
+      float tot[2][N][2] = {};
+      for (; chunks > 0; ++ch, --chunks, at.next(stages)) {
+        const uint8_t* st = ring + at.stage * C::kStage;
+        const uint8_t* rec = st + C::kW + 2 * C::kS;
+        ring_await(R, at);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int sb = warp + 8 * i;
-        if (16 * ch + sb >= nsub) break;
+        for (int i = 0; i < SUB; ++i) {
+          if (C::kSubs * ch + kw + 4 * i >= nsub) break;
+          uint4 b[N];
+          float2 dx[N];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int r = 16 * m + 2 * g;
-          uint32_t a[2][4];
-          load_tile(st + (sb >> 2) * (kStageW / 4), r, sb, t, a);
-          const uint8_t* sp = st + kStageW + (sb >> p.gsh) * 64 + 2 * r;
-          const float2 sc = load_pair<T>(sp), z8 = fold_zero(sc, load_pair<T>(sp + 1024));
-#pragma unroll
-          for (int tt = 0; tt < NT; ++tt) {
-            if (4 * tt >= n) break;
-            add_block(tot[m][tt], a, b[i][tt], sc, z8, dx[i][tt]);
-          }
-        }
-      }
-      ring_release(S.R, stages, f);
-      if (s + 1 == s1 || (s + 1) / nchunk != u) {   // the unit's last step here
-#pragma unroll
-        for (int tt = 0; tt < NT; ++tt) {
-          const int i = 4 * tt + t;                 // the lane's token
-          if (i < n) {
-            const float w = S.L.slot_w[start + i];
-            float* ap = acc + S.L.slot_token[start + i] * kRowsTile + 2 * g;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              ap[16 * m] = fmaf(w, tot[m][tt][0], ap[16 * m]);
-              ap[16 * m + 1] = fmaf(w, tot[m][tt][1], ap[16 * m + 1]);
-            }
+          for (int tt = 0; tt < N; ++tt) {
+            b[tt] = *reinterpret_cast<const uint4*>(rec + bq[tt] + i * kRecord);
+            dx[tt] = *reinterpret_cast<const float2*>(rec + bs[tt] + i * kRecord);
           }
 #pragma unroll
-          for (int m = 0; m < 2; ++m) tot[m][tt][0] = tot[m][tt][1] = 0.0f;
+          for (int m = 0; m < 2; ++m) {
+            const int r = 32 * rh + 16 * m + 2 * g;
+            uint32_t a[2][4];
+            load_tile(st + i * 64 * 128, r, kw, t, a);
+            const uint8_t* sp = st + C::kW + ((kw + 4 * i) >> p.gsh) * 128 + 2 * r;
+            const float2 sc = load_pair<T>(sp), z = load_pair<T>(sp + C::kS);
+#pragma unroll
+            for (int tt = 0; tt < N; ++tt) add_block(tot[m][tt], a, b[tt], sc, z, dx[tt]);
+          }
         }
-        __syncwarp();                               // another lane may hold this token in the next unit
+        ring_release(R, at);
       }
+#pragma unroll
+      for (int tt = 0; tt < N; ++tt) {
+        const int i = 4 * tt + t;                   // the lane's token
+        if (i < n) {
+          float2* ap = reinterpret_cast<float2*>(acc + L.slot_token[start + i] * kRowsTile);
+          const float2 v = ap[0], w = ap[8];
+          ap[0] = make_float2(v.x + tot[0][tt][0], v.y + tot[0][tt][1]);
+          ap[8] = make_float2(w.x + tot[1][tt][0], w.y + tot[1][tt][1]);
+        }
+      }
+      __syncwarp();                                 // another lane may hold this token in the next unit
+    };
+    for (int s = s0; s < s1;) {
+      const int u = s / nchunk, ch = s - u * nchunk, chunks = min(nchunk - ch, s1 - s);
+      const int n = L.unit_n[u];
+      if (NT == 1 || n <= 4) products(std::integral_constant<int, 1>(), u, ch, chunks);
+      else if (NT == 2 || n <= 8) products(std::integral_constant<int, NT < 2 ? 1 : 2>(), u, ch, chunks);
+      else products(std::integral_constant<int, NT>(), u, ch, chunks);
+      s += chunks;
     }
   }
   __syncthreads();
-  for (int i = tid; i < cells; i += kThreads) {
+  for (int i = tid; i < cells; i += C::kThreads) {
     float v = sums[i];
 #pragma unroll
-    for (int w = 1; w < kCons; ++w) v += sums[w * cells + i];
+    for (int w = 1; w < 4; ++w) v += sums[w * cells + i];
     sums[i] = v;
   }
   cluster_sync();
   const uint32_t base = smem_u32(sums);
-  for (int i = rank * kThreads + tid; i < cells; i += ranks * kThreads) {
+  for (int i = rank * C::kThreads + tid; i < cells; i += ranks * C::kThreads) {
     float v = 0.0f;
     for (uint32_t r = 0; r < ranks; ++r) v += ld_cluster_f32(mapa_shared(base + 4 * i, r));
     reinterpret_cast<T*>(p.out)[(int64_t)(i / kRowsTile) * p.K + n0 + i % kRowsTile] = awq::Traits<T>::fromf(v);

@@ -144,14 +144,23 @@ struct Choice {
 // memory. The slots that some token fills are numbered by (expert, token); a
 // unit is at most `cap` consecutive slots of one expert.
 struct Lists {
-  float slot_w[kMaxSlots];
-  uint16_t unit_expert[kMaxSlots];
-  uint16_t unit_start[kMaxSlots];
-  uint8_t unit_n[kMaxSlots];
-  uint8_t slot_token[kMaxSlots];
-  int warp_sum[32];
-  int n_units;
+  float* slot_w;
+  uint16_t *unit_expert, *unit_start;
+  uint8_t *unit_n, *slot_token;
+  int* scratch;                                      // [32], then the number of units
+  __device__ __forceinline__ int units() const { return scratch[32]; }
 };
+__host__ __device__ constexpr int lists_bytes(int slots) { return (144 + slots * 10 + 15) / 16 * 16; }
+__device__ __forceinline__ Lists lists_at(uint8_t* p, int slots) {
+  Lists L;
+  L.scratch = reinterpret_cast<int*>(p);
+  L.slot_w = reinterpret_cast<float*>(p + 144);
+  L.unit_expert = reinterpret_cast<uint16_t*>(L.slot_w + slots);
+  L.unit_start = L.unit_expert + slots;
+  L.unit_n = reinterpret_cast<uint8_t*>(L.unit_start + slots);
+  L.slot_token = L.unit_n + slots;
+  return L;
+}
 // What only the building of the lists needs; its memory may be used again afterwards.
 struct ListsTemp {
   unsigned long long mask[kMaxExperts];              // tokens of each expert
@@ -164,8 +173,8 @@ struct ListsTemp {
 // expert that a token names twice gets it once, with the sum of the two weights.
 // The order is fixed, so every CTA of both kernels builds the same lists.
 template <int THREADS>
-__device__ __forceinline__ void build_lists(const Choice& c, Lists& L, ListsTemp& tmp, int cap) {
-  static_assert(2 * THREADS >= kMaxExperts, "two experts a thread");
+__device__ __forceinline__ void build_lists(const Choice& c, const Lists& L, ListsTemp& tmp, int cap) {
+  constexpr int PER = (kMaxExperts + THREADS - 1) / THREADS;      // experts a thread
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e < c.E; e += THREADS) tmp.mask[e] = 0ull;
   const int slots = c.T * c.k;
@@ -190,10 +199,10 @@ __device__ __forceinline__ void build_lists(const Choice& c, Lists& L, ListsTemp
   for (int s = tid; s < slots; s += THREADS)
     if (tmp.id[s] >= 0) atomicOr(&tmp.mask[tmp.id[s]], 1ull << (s / c.k));
   __syncthreads();
-  int n[2], v = 0;
+  int n[PER], v = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * tid + i;
+  for (int i = 0; i < PER; ++i) {
+    const int e = PER * tid + i;
     n[i] = e < c.E ? __popcll(tmp.mask[e]) : 0;
     v += ((n[i] + cap - 1) / cap) << 16 | n[i];      // units and slots in one word: both at most kMaxSlots
   }
@@ -203,15 +212,15 @@ __device__ __forceinline__ void build_lists(const Choice& c, Lists& L, ListsTemp
     const int u = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += u;
   }
-  if (lane == 31) L.warp_sum[warp] = incl;
+  if (lane == 31) L.scratch[warp] = incl;
   __syncthreads();
   int before = 0;
-  for (int i = 0; i < warp; ++i) before += L.warp_sum[i];
+  for (int i = 0; i < warp; ++i) before += L.scratch[i];
   int unit = (before + incl - v) >> 16, slot = (before + incl - v) & 0xffff;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < PER; ++i) {
     if (n[i] == 0) continue;
-    const int e = 2 * tid + i;
+    const int e = PER * tid + i;
     for (int s = 0; s < n[i]; s += cap, ++unit) {
       L.unit_expert[unit] = (uint16_t)e;
       L.unit_start[unit] = (uint16_t)(slot + s);
@@ -226,7 +235,7 @@ __device__ __forceinline__ void build_lists(const Choice& c, Lists& L, ListsTemp
       L.slot_w[slot] = w;
     }
   }
-  if (tid == THREADS - 1) L.n_units = (before + incl) >> 16;
+  if (tid == THREADS - 1) L.scratch[32] = (before + incl) >> 16;
   fence_proxy_async_smem();                          // tmp may become the target of tensor copies
   __syncthreads();
 }
