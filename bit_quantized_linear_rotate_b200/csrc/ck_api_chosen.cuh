@@ -70,8 +70,9 @@ cudaError_t launch_gate_up(const ck::moe::Maps& maps, const ck::moe::Params& p, 
   const int offset = ring_offset(p.choice.T * p.choice.k, C::sums(p.choice.T, p.K));
   int ctas = C::kCtas;
   while (ctas > 1 && moe_stages(offset, C::kStage, ctas) == 0) --ctas;
-  const int stages = moe_stages(offset, C::kStage, ctas);
+  int stages = moe_stages(offset, C::kStage, ctas);
   if (stages == 0) return cudaErrorInvalidValue;
+  if (SELF) stages = std::min(stages, 3);   // leaves room for a CTA of down_kernel beside it
   const int smem = 1024 + offset + stages * C::kStage;
   const cudaError_t e = set_smem_max<Tag>(kern, smem, 227 * 1024);
   if (e != cudaSuccess) return e;
@@ -87,22 +88,24 @@ cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cud
   auto kern = down_kernel<T, NT, SUB>;
   struct Tag {};
   const int offset = ring_offset(p.choice.T * p.choice.k, C::sums(p.choice.T));
+  const int tiles = p.K / kRowsTile;
   int ctas = 3;
   while (ctas > 1 && moe_stages(offset, C::kStage, ctas) == 0) --ctas;
+  int cs = 8;
+  while (cs > 1 && tiles * cs > ctas * sm_count()) cs /= 2;
+  while (ctas > 1 && tiles * cs <= (ctas - 1) * sm_count()) --ctas;   // no more CTAs an SM than there are: deeper rings
+  if (p.lists == nullptr) ctas = 3;                                   // room beside gate_up_kernel's CTA
   const int stages = moe_stages(offset, C::kStage, ctas);
   if (stages == 0) return cudaErrorInvalidValue;
   const int smem = 1024 + offset + stages * C::kStage;
   const cudaError_t e = set_smem_max<Tag>(kern, smem, 227 * 1024);
   if (e != cudaSuccess) return e;
-  const int tiles = p.K / kRowsTile;
-  int cs = 8;
-  while (cs > 1 && tiles * cs > ctas * sm_count()) cs /= 2;
   return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, C::kThreads, smem, st, maps, p, stages);
 }
 
-// Workspace: x as fixed point, h as fixed point, the choice (prepare_kernel's).
+// Workspace: x as fixed point, h as fixed point, the lists.
 struct MoeWorkspace {
-  size_t xq, hq, ids, weights, total;
+  size_t xq, hq, lists, total;
   MoeWorkspace(int64_t T, int k, int64_t K, int64_t I) {
     size_t at = 0;
     auto take = [&at](int64_t bytes) {
@@ -112,47 +115,47 @@ struct MoeWorkspace {
     };
     xq = take(T * ck::moe::row_bytes((int)K));
     hq = take(T * k * ck::moe::row_bytes((int)I));
-    ids = take(T * k * 4);
-    weights = take(T * k * 4);
+    lists = take(ck::moe::lists_bytes((int)(T * k)));
     total = at;
   }
 };
 
-// Which kernels a call runs. One CTA an SM with 16 consumer warps and x converted by each CTA for
-// up to 4 tokens; else three CTAs an SM.
+// Which kernels a call runs. Up to 4 tokens: 16 consumer warps, one CTA an SM, which routes and
+// converts x itself. Else three CTAs an SM, and token tiles (of four) a unit by how many
+// tokens an expert is likely to get, the mean and three standard deviations: an expert with
+// more is read again for the rest, while room for 16 tokens in every stage costs depth of the ring.
 bool moe_self(const ck::moe::Params& p) {
-  return p.choice.T <= ck::moe::kSelfTokens && p.choice.T * ck::moe::row_bytes(p.K) <= ck::moe::kSelfBytes;
+  return p.choice.T <= ck::moe::kFewTokens && p.choice.T * ck::moe::row_bytes(p.K) <= ck::moe::kSelfBytes;
+}
+int moe_token_tiles(const ck::moe::Params& p) {
+  const double mean = (double)p.choice.T * p.choice.k / p.choice.E;
+  const double likely = std::min<double>(p.choice.T, mean + 3 * std::sqrt(mean));
+  return likely <= 4 ? 1 : likely <= 8 ? 2 : 4;
 }
 int gate_up_stage_cols(const ck::moe::Params& p) { return moe_self(p) ? 512 : 256; }
-int down_stage_cols(const ck::moe::Params& p) { return p.choice.T <= 8 ? 512 : 256; }
+int down_stage_cols(const ck::moe::Params& p) { return moe_token_tiles(p) <= 2 ? 512 : 256; }
 
 template <typename T>
 cudaError_t launch_moe(const ck::moe::Maps& gate_up, const ck::moe::Maps& down, ck::moe::Params& p, uint8_t* ws,
                        const MoeWorkspace& w, cudaStream_t st) {
   using namespace ck::moe;
-  const int tokens = p.choice.T;
+  const int tiles = moe_token_tiles(p);
   cudaError_t e;
   if (moe_self(p)) {
+    p.lists = nullptr;
     e = launch_gate_up<T, 1, 4, true>(gate_up, p, st);
   } else {
-    const bool route = p.choice.ids == nullptr;
-    int32_t* ids = reinterpret_cast<int32_t*>(ws + w.ids);
-    float* weights = reinterpret_cast<float*>(ws + w.weights);
-    e = launch_pdl(prepare_kernel<T>, dim3((unsigned)tokens), dim3(kPrepThreads), 0, st, p, route ? ids : nullptr,
-                   weights);
+    p.lists = ws + w.lists;
+    e = launch_pdl(prepare_kernel<T>, dim3((unsigned)p.choice.T + 1), dim3(kPrepThreads), 0, st, p, 4 * tiles);
     if (e != cudaSuccess) return e;
-    if (route) {
-      p.choice.ids = ids;
-      p.choice.weights = weights;
-    }
-    if (tokens <= 4) e = launch_gate_up<T, 1, 2, false>(gate_up, p, st);
-    else if (tokens <= 8) e = launch_gate_up<T, 2, 2, false>(gate_up, p, st);
-    else e = launch_gate_up<T, 4, 2, false>(gate_up, p, st);
+    e = tiles == 1 ? launch_gate_up<T, 1, 2, false>(gate_up, p, st)
+      : tiles == 2 ? launch_gate_up<T, 2, 2, false>(gate_up, p, st)
+                   : launch_gate_up<T, 4, 2, false>(gate_up, p, st);
   }
   if (e != cudaSuccess) return e;
-  if (tokens <= 4) return launch_down<T, 1, 2>(down, p, st);
-  if (tokens <= 8) return launch_down<T, 2, 2>(down, p, st);
-  return launch_down<T, 4, 1>(down, p, st);
+  return tiles == 1 ? launch_down<T, 1, 2>(down, p, st)
+       : tiles == 2 ? launch_down<T, 2, 2>(down, p, st)
+                    : launch_down<T, 4, 1>(down, p, st);
 }
 
 // Maps of `rows` weight rows of `cols` columns for each expert: boxes of 64

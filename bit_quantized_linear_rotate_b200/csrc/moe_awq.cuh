@@ -57,6 +57,7 @@ struct Params {
   int K, I, gsh;                       // quantization group of sub-block sb: sb >> gsh
   uint8_t* xq;                         // (T) rows of x by prepare_kernel; unused where a CTA converts x itself
   uint8_t* hq;                         // (slots) rows of h
+  uint8_t* lists;                      // by prepare_kernel (lists_at)
   void* out;                           // (T, K) T
 };
 
@@ -126,26 +127,24 @@ __device__ __forceinline__ void convert_row(const T* x, int K, uint8_t* row, int
 
 // ----------------------------------------------------------- prepare (T > 4)
 
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 512;
 
-// One CTA a token: its row of x as fixed point, and (logits given) its choice.
+// CTA t < T: token t's row of x as fixed point. CTA T: the choice and its lists.
 template <typename T>
-__global__ void __launch_bounds__(kPrepThreads)
-    prepare_kernel(const Params p, int32_t* __restrict__ ids, float* __restrict__ weights) {
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Params p, int cap) {
+  __shared__ ListsTemp tmp;
+  __shared__ __align__(16) uint8_t block[lists_bytes(kMaxSlots)];
   grid_dep_wait();
   grid_dep_launch();
-  const int t = blockIdx.x;
-  convert_row<T, kPrepThreads>(reinterpret_cast<const T*>(p.x) + t * p.ldx, p.K, p.xq + (int64_t)t * row_bytes(p.K),
-                               threadIdx.x);
-  if (ids != nullptr && threadIdx.x < 32) {
-    int id;
-    float w;
-    choose_any(p.choice.logits, p.choice.ldt, t, p.choice.E, p.choice.k, p.choice.renorm != 0, id, w);
-    if ((int)threadIdx.x < p.choice.k) {
-      ids[t * p.choice.k + threadIdx.x] = id;
-      weights[t * p.choice.k + threadIdx.x] = w;
-    }
+  const int t = blockIdx.x, slots = p.choice.T * p.choice.k;
+  if (t < p.choice.T) {
+    convert_row<T, kPrepThreads>(reinterpret_cast<const T*>(p.x) + t * p.ldx, p.K, p.xq + (int64_t)t * row_bytes(p.K),
+                                 threadIdx.x);
+    return;
   }
+  build_lists<kPrepThreads>(p.choice, lists_at(block, slots), tmp, cap);
+  for (int i = threadIdx.x; i < lists_bytes(slots) / 16; i += kPrepThreads)
+    reinterpret_cast<uint4*>(p.lists)[i] = reinterpret_cast<const uint4*>(block)[i];
 }
 
 // ------------------------------------------------------------- weight tiles
@@ -259,7 +258,7 @@ __device__ __forceinline__ void consumers_sync() {
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // Shared memory of both kernels: the ring's barriers, the lists, what the kernel sums in, and
-// the ring (1024-byte aligned stages), whose memory the building of the lists uses first.
+// the ring (1024-byte aligned stages).
 constexpr int kHead = (sizeof(Ring) + 127) / 128 * 128;
 __host__ __device__ constexpr int ring_offset(int slots, int sums) {
   return (kHead + (lists_bytes(slots) + 127) / 128 * 128 + sums + 1023) / 1024 * 1024;
@@ -270,15 +269,16 @@ __device__ __forceinline__ uint8_t* align_1024(uint8_t* p) { return p + ((1024 -
 // -------------------------------------------------------------- gate and up
 
 // An item is 64 columns of h of one unit (an expert's tokens, at most 4 NT): 64
-// gate rows and the 64 up rows that belong to them. A CTA takes a contiguous
-// share of the items and streams their weights, with the unit's rows of x, 128 KW
-// columns a stage. Consumer warp (kw, rq) multiplies 16 gate and 16 up rows with sub-blocks kw
+// gate rows and the 64 up rows that belong to them. A CTA takes every gridDim.x-th
+// item, so that units of many and of few tokens mix (in contiguous shares some CTAs
+// ran for 45 us and others for 128), and streams its weights, with the unit's rows of x,
+// 128 KW columns a stage. Consumer warp (kw, rq) multiplies 16 gate and 16 up rows with sub-blocks kw
 // and kw + KW of each stage; the KW partial sums meet in shared memory, where
 // one warp a token forms h and converts it to fixed point.
 //
-// SELF: every CTA converts x itself, into shared memory (T <= kSelfTokens): the launch of
-// prepare_kernel and the wait for it cost more.
-constexpr int kSelfTokens = 4, kSelfBytes = 64 * 1024;
+// SELF: every CTA routes and converts x itself, into shared memory (T <= kFewTokens): the
+// launch of prepare_kernel and the wait for it cost more.
+constexpr int kSelfBytes = 32 * 1024;
 
 template <int NT, int KW, bool SELF>
 struct GateUp {
@@ -290,6 +290,7 @@ struct GateUp {
   static constexpr int kRows = SELF ? 0 : 4 * NT * (kSubs / 4) * kRecord;
   static constexpr int kStage = (2 * kW + 4 * kS + kRows + 1023) / 1024 * 1024;
   static constexpr int kRed = KW * 4 * 2 * NT * 32 * 8;         // float2 [kw][rq][gate, up][token tile][lane]
+  static_assert(sizeof(FewTemp) <= kRed, "build_few works in it");
   __host__ __device__ static constexpr int sums(int T, int K) { return kRed + (SELF ? T * row_bytes(K) : 0); }
 };
 
@@ -315,12 +316,11 @@ __global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW,
   }
   grid_dep_wait();
   grid_dep_launch();   // after the wait: the next kernel may read the choice before its own wait
-  static_assert(sizeof(ListsTemp) <= 2 * C::kStage, "the lists are built in the ring's memory");
-  build_lists<C::kThreads>(p.choice, L, *reinterpret_cast<ListsTemp*>(ring), 4 * NT);
+  if constexpr (SELF) build_few(p.choice, L, *reinterpret_cast<FewTemp*>(red));
+  else copy_lists<C::kThreads>(sm + kHead, p.lists, slots);
 
   const int per_unit = p.I / kColsItem, nsub = p.K >> 6, nchunk = (nsub + C::kSubs - 1) / C::kSubs;
-  const int64_t items = (int64_t)L.units() * per_unit;
-  const int i0 = (int)(items * blockIdx.x / gridDim.x), i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  const int items = L.units() * per_unit;
   const int srows = C::kSubs >> p.gsh;   // rows of scales a stage: its columns' groups
   const int xrow = row_bytes(p.K);
 
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW,
     Cursor at;
     int issued = 0;
     bool live = true;
-    for (int item = i0; item < i1 && live; ++item) {
+    for (int item = blockIdx.x; item < items && live; item += gridDim.x) {
       const int u = item / per_unit, c0 = (item % per_unit) * kColsItem;
       const int e = L.unit_expert[u], row = e * 2 * p.I + c0, n = L.unit_n[u];
       const uint8_t* xr = nullptr;
@@ -421,13 +421,13 @@ __global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW,
     }
   };
 
-  for (int item = i0; item < i1; ++item) {
+  for (int item = blockIdx.x, turn = 0; item < items; item += gridDim.x, ++turn) {
     const int u = item / per_unit, cb = item % per_unit;
     const int start = L.unit_start[u], n = L.unit_n[u], nt = (n + 3) >> 2;
     if (NT == 1 || n <= 4) products(std::integral_constant<int, 1>(), start, n);
     else if (NT == 2 || n <= 8) products(std::integral_constant<int, NT < 2 ? 1 : 2>(), start, n);
     else products(std::integral_constant<int, NT>(), start, n);
-    if (item != i0) consumers_sync<32 * C::kCons>();   // the previous item's sums have been read
+    if (turn != 0) consumers_sync<32 * C::kCons>();   // the previous item's sums have been read
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW,
         if (tt < nt) red[((warp * 2 + m) * NT + tt) * 32 + lane] = make_float2(tot[m][tt][0], tot[m][tt][1]);
     consumers_sync<32 * C::kCons>();
     // Token c of the unit: a lane forms columns 2 lane and 2 lane + 1. The other warps go on.
-    for (int c = (warp + item) & (C::kCons - 1); c < n; c += C::kCons) {
+    for (int c = (warp + turn) & (C::kCons - 1); c < n; c += C::kCons) {
       const int ln = (lane & 7) * 4 + (c & 3);
       float2 gate = make_float2(0.0f, 0.0f), up = gate;
 #pragma unroll
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW,
 // --------------------------------------------------------------------- down
 
 // A cluster of CTAs owns 64 output columns and walks (unit, 256 SUB columns of h)
-// steps, each CTA a contiguous share of them; consumer warp (kw, rh) takes sub-blocks
+// steps, each CTA a share of them; consumer warp (kw, rh) takes sub-blocks
 // kw (and kw + 4) of a step and 32 of the output columns. When the unit changes, each warp
 // adds its sums to the accumulator (T, 64) that it shares with the other rh; at the
 // end the four accumulators and then the CTAs' are added in order. The weights of
@@ -505,21 +505,33 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
     ring_init(R, stages, C::kCons);
   }
   for (int i = tid; i < 4 * cells; i += C::kThreads) sums[i] = 0.0f;
-  // The choice was complete before gate_up_kernel let this kernel start.
-  static_assert(sizeof(ListsTemp) <= 2 * C::kStage, "the lists are built in the ring's memory");
-  build_lists<C::kThreads>(p.choice, L, *reinterpret_cast<ListsTemp*>(ring), 4 * NT);
+  // The choice and the lists were complete before gate_up_kernel let this kernel start.
+  if (p.lists == nullptr) build_few(p.choice, L, *reinterpret_cast<FewTemp*>(ring));
+  else copy_lists<C::kThreads>(sm + kHead, p.lists, slots);
 
   const int nsub = p.I >> 6, nchunk = (nsub + C::kSubs - 1) / C::kSubs;
-  const int64_t steps = (int64_t)L.units() * nchunk;
-  const int s0 = (int)(steps * rank / ranks), s1 = (int)(steps * (rank + 1) / ranks);
   const int srows = C::kSubs >> p.gsh;
   const int hrow = row_bytes(p.I);
+  // This CTA's steps: with many chunks a unit, every ranks-th chunk of each unit (units of many
+  // and of few tokens mix); else a contiguous share.
+  const int units = L.units();
+  int u0 = 0, ch0 = (int)rank, stride = (int)ranks, left;
+  if (nchunk >= 2 * (int)ranks) {
+    left = units * ((nchunk - (int)rank + (int)ranks - 1) / (int)ranks);
+  } else {
+    const int steps = units * nchunk, s0 = (int)((int64_t)steps * rank / ranks);
+    left = (int)((int64_t)steps * (rank + 1) / ranks) - s0;
+    u0 = s0 / nchunk;
+    ch0 = s0 - u0 * nchunk;
+    stride = 1;
+  }
+  const int again = stride == 1 ? 0 : ch0;           // the first chunk of the next unit
 
   if (warp == C::kCons) {
     const int ngrp = nsub >> p.gsh;
-    // Weights and scales of step s, and the bytes of its rows of h announced.
-    auto fetch_weights = [&](int s, const Cursor& at) {
-      const int u = s / nchunk, ch = s - u * nchunk, e = L.unit_expert[u];
+    // Weights and scales of a step, and the bytes of its rows of h announced.
+    auto fetch_weights = [&](int u, int ch, const Cursor& at) {
+      const int e = L.unit_expert[u];
       uint8_t* st = ring + at.stage * C::kStage;
       uint64_t* bar = &R.full[at.stage];
       const int boxes = min(SUB, (nsub - C::kSubs * ch + 3) >> 2);
@@ -529,32 +541,37 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
       tma_load_2d(st + C::kW, &maps.s, bar, n0, e * ngrp + ch * srows);
       tma_load_2d(st + C::kW + C::kS, &maps.z, bar, n0, e * ngrp + ch * srows);
     };
-    auto fetch_rows = [&](int s, const Cursor& at) {
-      const int u = s / nchunk, ch = s - u * nchunk;
+    auto fetch_rows = [&](int u, int ch, const Cursor& at) {
       const int boxes = min(SUB, (nsub - C::kSubs * ch + 3) >> 2);
       if (lane < L.unit_n[u])
         bulk_load(ring + at.stage * C::kStage + C::kW + 2 * C::kS + lane * SUB * kRecord,
                   p.hq + (int64_t)(L.unit_start[u] + lane) * hrow + ch * SUB * kRecord, boxes * kRecord,
                   &R.full[at.stage]);
     };
-    const int ahead = min(stages, s1 - s0);
+    const int ahead = min(stages, left);
     Cursor at;
+    int u = u0, ch = ch0;
+    auto step = [&] {
+      at.next(stages);
+      if ((ch += stride) >= nchunk) ch = again, ++u;
+    };
     if (lane == 0)
-      for (int i = 0; i < ahead; ++i, at.next(stages)) fetch_weights(s0 + i, at);
+      for (int i = 0; i < ahead; ++i, step()) fetch_weights(u, ch, at);
     __syncwarp();
     grid_dep_wait();
     grid_dep_launch();
     fence_proxy_async_all();
     at = Cursor();
-    for (int i = 0; i < ahead; ++i, at.next(stages)) fetch_rows(s0 + i, at);
+    u = u0, ch = ch0;
+    for (int i = 0; i < ahead; ++i, step()) fetch_rows(u, ch, at);
     int issued = ahead;
     bool live = true;
-    for (int s = s0 + ahead; s < s1; ++s, ++issued, at.next(stages)) {
+    for (; issued < left; ++issued, step()) {
       live = __all_sync(0xffffffffu, ring_claim(R, at));
       if (!live) break;
-      if (lane == 0) fetch_weights(s, at);
+      if (lane == 0) fetch_weights(u, ch, at);
       __syncwarp();
-      fetch_rows(s, at);
+      fetch_rows(u, ch, at);
     }
     if (!live && lane == 0) ring_drain(R, at, stages, issued);
   } else {
@@ -574,7 +591,7 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
         bs[tt] = min(4 * tt + t, n - 1) * SUB * kRecord + 512 + kw * 8;
       }
       float tot[2][N][2] = {};
-      for (; chunks > 0; ++ch, --chunks, at.next(stages)) {
+      for (; chunks > 0; ch += stride, --chunks, at.next(stages)) {
         const uint8_t* st = ring + at.stage * C::kStage;
         const uint8_t* rec = st + C::kW + 2 * C::kS;
         ring_await(R, at);
@@ -613,13 +630,13 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
       }
       __syncwarp();                                 // another lane may hold this token in the next unit
     };
-    for (int s = s0; s < s1;) {
-      const int u = s / nchunk, ch = s - u * nchunk, chunks = min(nchunk - ch, s1 - s);
+    for (int u = u0, ch = ch0; left > 0; ++u, ch = again) {
+      const int chunks = min((nchunk - ch + stride - 1) / stride, left);
       const int n = L.unit_n[u];
       if (NT == 1 || n <= 4) products(std::integral_constant<int, 1>(), u, ch, chunks);
       else if (NT == 2 || n <= 8) products(std::integral_constant<int, NT < 2 ? 1 : 2>(), u, ch, chunks);
       else products(std::integral_constant<int, NT>(), u, ch, chunks);
-      s += chunks;
+      left -= chunks;
     }
   }
   __syncthreads();
