@@ -24,6 +24,7 @@
 #include "gemv_w4a8_stream.cuh"
 #include "gemv_w4a8_tc.cuh"
 #include "lora_add.cuh"
+#include "lora_tc.cuh"
 #include "moe_awq.cuh"
 #include "rotate_quant.cuh"
 #include "rotate_quant_general.cuh"

@@ -243,6 +243,27 @@ cudaError_t launch_lora_tm(const ck::lora::Params& p, int64_t tiles, cudaStream_
   return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kThreads, sizeof(SM), st, p);
 }
 
+template <typename T, typename TY, int RB>
+cudaError_t launch_lora_tc(const ck::lora::Params& p, int64_t tiles, cudaStream_t st) {
+  using namespace ck::lora;
+  using C = LoraTc<RB>;
+  auto kern = lora_tc_kernel<T, TY, RB>;
+  struct Tag {};
+  const cudaError_t e = set_smem_max<Tag>(kern, C::kSmem, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap a, b;   // A in boxes of 64 k x R (rounded up) rows, B in boxes of 64 ranks x 128 rows
+  if (make_tmap(&a, p.a, (uint64_t)p.K, (uint64_t)p.L * p.R, (uint64_t)p.K * 2, 64, (uint32_t)((p.R + 15) / 16 * 16),
+                CU_TENSOR_MAP_SWIZZLE_128B, dt) != CK_OK ||
+      make_tmap(&b, p.b, (uint64_t)p.R, (uint64_t)p.L * p.N, (uint64_t)p.R * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B,
+                dt) != CK_OK)
+    return cudaErrorInvalidValue;
+  int cs = 8;
+  while (cs > 1 && tiles * cs > C::kCtas * sm_count()) cs /= 2;
+  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kTcThreads, C::kSmem, st, a, b, p);
+}
+
 template <typename T, typename TY>
 cudaError_t launch_lora(const ck::lora::Params& p, int tm, int64_t tiles, cudaStream_t st) {
   if (tm == 16) {
@@ -250,13 +271,13 @@ cudaError_t launch_lora(const ck::lora::Params& p, int tm, int64_t tiles, cudaSt
     if (p.R <= 64) return launch_lora_tm<T, TY, 2, 16>(p, tiles, st);
     return launch_lora_tm<T, TY, 4, 16>(p, tiles, st);
   }
-  if (p.R <= 32) return launch_lora_tm<T, TY, 1, 64>(p, tiles, st);
-  if (p.R <= 64) return launch_lora_tm<T, TY, 2, 64>(p, tiles, st);
-  return launch_lora_tm<T, TY, 4, 64>(p, tiles, st);
+  return p.R <= 64 ? launch_lora_tc<T, TY, 1>(p, tiles, st) : launch_lora_tc<T, TY, 2>(p, tiles, st);
 }
 
 // Tokens of a tile, by how many tokens an adapter has on average.
-int lora_tile(int64_t M, int64_t L) { return M >= 512 && M >= 16 * L ? 64 : 16; }
+int lora_tile(int64_t M, int64_t L) {
+  return M > ck::lora::kSelfGroup && M >= 32 * L ? ck::lora::kTcTokens : 16;
+}
 
 }  // namespace
 
@@ -344,7 +365,7 @@ ck_status ck_lora_add(const void* y, ck_dtype yt, const void* x, ck_dtype xt, in
   if (K % 8 != 0) return fail(CK_ERR_UNSUPPORTED, "%s: K=%lld must be a multiple of 8", who, (long long)K);
   if (L > ck::lora::kMaxAdapters)
     return fail(CK_ERR_UNSUPPORTED, "%s: L=%lld > %d", who, (long long)L, ck::lora::kMaxAdapters);
-  if (K > INT32_MAX / 2 || N > INT32_MAX / 2 || M > (int64_t)1 << 26)
+  if (K > INT32_MAX / 2 || N > INT32_MAX / 2 || L * N > INT32_MAX || M > (int64_t)1 << 26)
     return fail(CK_ERR_UNSUPPORTED, "%s: dimension too large", who);
   if (M == 0) return ok();
   if (ldx < K || ldx % 8 != 0)

@@ -169,6 +169,37 @@ template <typename T> struct Half2Of;
 template <> struct Half2Of<__nv_bfloat16> { static constexpr bool kScaled = false; };
 template <> struct Half2Of<__half> { static constexpr bool kScaled = true; };
 
+// The power of two that brings a row's largest magnitude (its bits) to [2^13, 2^14); 0 where it is zero,
+// subnormal or not finite.
+__device__ __forceinline__ int scale_exponent(uint32_t top) {
+  const int e = (int)(top >> 23);
+  return e > 0 && e < 255 ? max(-100, min(100, 13 - (e - 127))) : 0;
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// v as hi + lo; an infinity stays one.
+template <typename T>
+__device__ __forceinline__ void split(float v, T& hi, T& lo) {
+  hi = awq::Traits<T>::fromf(v);
+  const float h = awq::Traits<T>::tof(hi);
+  lo = awq::Traits<T>::fromf(isfinite(h) ? v - h : 0.0f);
+}
+
+// Columns [c0, c1) of y's rows token[0 .. n) into out (nothing where out is y).
+template <typename TY>
+__device__ __forceinline__ void copy_rows(const TY* y, TY* out, const Params& p, const int* token, int n, int c0, int c1,
+                                          int warp, int warps, int lane) {
+  if (y == out) return;
+  for (int m = warp; m < n; m += warps) {
+    const TY* yp = y + token[m] * p.ldy;
+    TY* op = out + token[m] * p.ldo;
+    if (p.vec)
+      for (int c = c0 + 8 * lane; c < c1; c += 256) *reinterpret_cast<uint4*>(op + c) = *reinterpret_cast<const uint4*>(yp + c);
+    else
+      for (int c = c0 + lane; c < c1; c += 32) op[c] = yp[c];
+  }
+}
+
 // Shared memory of a CTA: RC 32-wide chunks of rank, TM tokens.
 template <int RC, int TM>
 struct Smem {
@@ -205,18 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
   const int nb0 = (int)((int64_t)nb * rank / ranks), nb1 = (int)((int64_t)nb * (rank + 1) / ranks);
 
   if (adapter < 0) {                                  // tokens without an adapter
-    if (y != out) {
-      const int c0 = 32 * nb0, c1 = min(32 * nb1, p.N);
-      for (int m = warp; m < n; m += kWarps) {
-        const TY* yp = y + S.token[m] * p.ldy;
-        TY* op = out + S.token[m] * p.ldo;
-        if (p.vec)
-          for (int c = c0 + 8 * lane; c < c1; c += 256)
-            *reinterpret_cast<uint4*>(op + c) = *reinterpret_cast<const uint4*>(yp + c);
-        else
-          for (int c = c0 + lane; c < c1; c += 32) op[c] = yp[c];
-      }
-    }
+    copy_rows(y, out, p, S.token, n, 32 * nb0, min(32 * nb1, p.N), warp, kWarps, lane);
     return;
   }
 
@@ -286,20 +306,17 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < RC; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-      top = __reduce_max_sync(0xffffffffu, top) >> 23;              // the largest exponent
-      if (top > 0 && top < 255) ex = max(-100, min(100, 13 - ((int)top - 127)));
+      ex = scale_exponent(__reduce_max_sync(0xffffffffu, top));
     }
-    const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+    const float up = exp2_int(ex);
 #pragma unroll
     for (int i = 0; i < RC; ++i) {
-      const float s = v[i] * up;
-      const T h = Tr::fromf(s);
-      const float hf = Tr::tof(h);
-      const T l = Tr::fromf(isfinite(hf) ? s - hf : 0.0f);          // an infinity stays one
+      T h, l;
+      split(v[i] * up, h, l);
       S.hi[m][32 * i + lane] = *reinterpret_cast<const uint16_t*>(&h);
       S.lo[m][32 * i + lane] = *reinterpret_cast<const uint16_t*>(&l);
     }
-    if (lane == 0) S.row_scale[m] = as * __uint_as_float((uint32_t)(127 - ex) << 23);
+    if (lane == 0) S.row_scale[m] = as * exp2_int(-ex);
   }
   __syncthreads();
 

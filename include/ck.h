@@ -451,7 +451,8 @@ ck_status ck_moe_experts_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_
  * lora_a : (L, R, K) xt, lora_b : (L, N, R) xt, contiguous, 16-byte aligned. Adapters
  *          of lower rank are padded with zeros.
  * ids    : (M) int32, any order. scales : (L) float32, or NULL for 1.
- * R a multiple of 8 up to 128, K % 8 == 0, L <= 8192, M <= 2^26 (0: no-op).
+ * R a multiple of 8 up to 128, K % 8 == 0, L <= 8192, L * N < 2^31, M <= 2^26
+ *          (0: no-op).
  * workspace : at least ck_lora_add_workspace_bytes(M, L) bytes, 256-byte aligned
  *          (NULL where that is 0), belongs to the call until it has run.
  */
