@@ -259,8 +259,17 @@ cudaError_t launch_lora_tc(const ck::lora::Params& p, int64_t tiles, cudaStream_
       make_tmap(&b, p.b, (uint64_t)p.R, (uint64_t)p.L * p.N, (uint64_t)p.R * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B,
                 dt) != CK_OK)
     return cudaErrorInvalidValue;
-  int cs = 8;
-  while (cs > 1 && tiles * cs > C::kCtas * sm_count()) cs /= 2;
+  // The cluster size by the time it is expected to take: rounds of one CTA an SM, each 1 / cs of a tile's
+  // bytes (at an SM's 43 GB/s) and 6 us for the stages that wait for one another; the number of
+  // tiles, known on the device only, as the full ones and half of the adapters' last ones.
+  const double work = 128.0 * (p.K + 2.0 * p.N) * 2 / 43e3, fixed = 6.0;
+  const double likely = (double)p.M / kTcTokens + std::min<double>(p.L + 1, (double)p.M / kTcTokens) / 2;
+  int cs = 1;
+  double best = 1e30;
+  for (int c = 1; c <= 8; c *= 2) {
+    const double t = std::ceil(likely * c / sm_count()) * (work / c + fixed);
+    if (t < best) best = t, cs = c;
+  }
   return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kTcThreads, C::kSmem, st, a, b, p);
 }
 

@@ -62,7 +62,40 @@ __host__ __device__ inline int64_t max_tiles(int64_t M, int64_t L, int tm) {
 }
 
 // Sorts the tokens of a large batch by adapter: tile list and token order, by one CTA. Bucket L
-// holds the tokens without an adapter.
+// holds the tokens without an adapter. A thread takes eight consecutive tokens at a time, read
+// before any is counted (one at a time the two passes over 8192 ids took 7.6 us): prompts are
+// runs of one id, so a warp mostly counts 256 tokens with one atomic.
+constexpr int kGroupEach = 8;
+
+// The buckets of tokens i0 .. i0 + 7; -1 past the last.
+__device__ __forceinline__ void load_buckets(const int32_t* ids, int64_t i0, int M, int L, int (&a)[kGroupEach]) {
+  const bool wide = (reinterpret_cast<uintptr_t>(ids) & 15) == 0 && i0 + kGroupEach <= M;
+  if (wide) {
+    const int4 v = *reinterpret_cast<const int4*>(ids + i0), w = *reinterpret_cast<const int4*>(ids + i0 + 4);
+    a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w, a[4] = w.x, a[5] = w.y, a[6] = w.z, a[7] = w.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kGroupEach; ++j) a[j] = i0 + j < M ? ids[i0 + j] : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < kGroupEach; ++j) a[j] = i0 + j >= M ? -1 : a[j] >= 0 && a[j] < L ? a[j] : L;
+}
+
+// Adds each token to its bucket's counter; at[j]: the counter before token j (by a whole warp).
+__device__ __forceinline__ void take_places(int* count, const int (&a)[kGroupEach], int (&at)[kGroupEach]) {
+  const int lane = threadIdx.x & 31;
+  bool one = a[0] >= 0;
+#pragma unroll
+  for (int j = 1; j < kGroupEach; ++j) one = one && a[j] == a[0];
+  const unsigned same = __match_any_sync(0xffffffffu, one ? a[0] : -1 - lane);
+  const int leader = __ffs(same) - 1;
+  int base = 0;
+  if (one && lane == leader) base = atomicAdd(&count[a[0]], kGroupEach * __popc(same));
+  base = __shfl_sync(0xffffffffu, base, leader) + kGroupEach * __popc(same & ((1u << lane) - 1));
+#pragma unroll
+  for (int j = 0; j < kGroupEach; ++j) at[j] = one ? base + j : a[j] >= 0 ? atomicAdd(&count[a[j]], 1) : 0;
+}
+
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __restrict__ ids, int M, int L, int tm,
                                                               int max_tiles, int32_t* __restrict__ tiles,
                                                               int32_t* __restrict__ order) {
@@ -70,16 +103,18 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
   __shared__ int warp_sum[2][kGroupThreads / 32];
   __shared__ int carry[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kRound = kGroupThreads * kGroupEach;
+  const int rounds = (M + kRound - 1) / kRound;
   for (int i = tid; i <= L; i += kGroupThreads) count[i] = 0;
   if (tid == 0) carry[0] = carry[1] = 0;
   grid_dep_wait();
   grid_dep_launch();
+  int a[kGroupEach], at[kGroupEach];
+  load_buckets(ids, kGroupEach * tid, M, L, a);
   __syncthreads();
-  for (int i = tid; i < (M + 31) / 32 * 32; i += kGroupThreads) {
-    int a = i < M ? ids[i] : -2;
-    if (i < M && (a < 0 || a >= L)) a = L;
-    const unsigned same = __match_any_sync(0xffffffffu, a);
-    if (a >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[a], __popc(same));
+  for (int r = 0; r < rounds; ++r) {
+    if (r > 0) load_buckets(ids, (int64_t)kRound * r + kGroupEach * tid, M, L, a);
+    take_places(count, a, at);
   }
   __syncthreads();
   for (int b0 = 0; b0 <= L; b0 += kGroupThreads) {   // running sums of tokens and of tiles
@@ -94,31 +129,28 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
     if (lane == 31) warp_sum[0][warp] = in, warp_sum[1][warp] = it;
     __syncthreads();
     int bn = carry[0], bt = carry[1];
-    for (int w = 0; w < warp; ++w) bn += warp_sum[0][w], bt += warp_sum[1][w];
+    if (b0 + 32 * warp <= L)                         // warps without a bucket need no sums
+      for (int w = 0; w < warp; ++w) bn += warp_sum[0][w], bt += warp_sum[1][w];
     const int start = bn + in - n;
     int tile = bt + it - nt;
     if (b <= L) {
       count[b] = start;
-      for (int s = 0; s < n; s += tm, ++tile) {
-        int4 v = make_int4(b < L ? b : -1, start + s, min(tm, n - s), 0);
-        reinterpret_cast<int4*>(tiles)[tile] = v;
-      }
+      for (int s = 0; s < n; s += tm, ++tile)
+        reinterpret_cast<int4*>(tiles)[tile] = make_int4(b < L ? b : -1, start + s, min(tm, n - s), 0);
     }
     __syncthreads();
-    if (tid == kGroupThreads - 1) carry[0] = bn + in, carry[1] = bt + it;
+    if (b == min(L, b0 + kGroupThreads - 1)) carry[0] = bn + in, carry[1] = bt + it;
     __syncthreads();
   }
   for (int i = carry[1] + tid; i < max_tiles; i += kGroupThreads)   // tiles that this batch has not
     reinterpret_cast<int4*>(tiles)[i] = make_int4(-1, 0, 0, 0);
-  for (int i = tid; i < (M + 31) / 32 * 32; i += kGroupThreads) {
-    int a = i < M ? ids[i] : -2;
-    if (i < M && (a < 0 || a >= L)) a = L;
-    const unsigned same = __match_any_sync(0xffffffffu, a);
-    const int leader = __ffs(same) - 1;
-    int at = 0;
-    if (a >= 0 && lane == leader) at = atomicAdd(&count[a], __popc(same));
-    at = __shfl_sync(0xffffffffu, at, leader);
-    if (a >= 0) order[at + __popc(same & ((1u << lane) - 1))] = i;
+  for (int r = 0; r < rounds; ++r) {
+    const int64_t i0 = (int64_t)kRound * r + kGroupEach * tid;
+    if (rounds > 1) load_buckets(ids, i0, M, L, a);
+    take_places(count, a, at);
+#pragma unroll
+    for (int j = 0; j < kGroupEach; ++j)
+      if (a[j] >= 0) order[at[j]] = (int)i0 + j;
   }
 }
 

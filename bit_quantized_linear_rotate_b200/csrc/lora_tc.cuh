@@ -14,14 +14,16 @@
 // units to x, y and out; with mma.sync fragments straight from global
 // memory the M = 8192, R = 64 case took 190 us.
 //
-// Warps 0-7 bring x in (16-byte asynchronous copies: a tile's tokens may be any rows), later
-// reduce v and write the output; warp 8 brings in A and B by tensor copies (rows of
-// another adapter and zeros past the end fill what R leaves of a block); warp 9 issues
-// the MMAs. Accumulators: 256 TMEM columns, so that two CTAs share an SM.
+// Warps 0-15 bring x in (16-byte asynchronous copies: a tile's tokens may be any rows), later
+// reduce v, bring in y and write the output; warp 16 brings in A and B by tensor copies
+// (rows of another adapter and zeros past the end fill what R leaves of a block); warp 17
+// issues the MMAs.
 //
 // Shared memory, one area used twice (LoraTc): the shrink's stages, then the partial sums of v,
-// v as operands and the ring of B. All barrier waits are bounded; after a timeout the CTA
-// runs on without waiting, so that its cluster's barriers are met.
+// v as operands, the ring of B and the ring of y. One CTA an SM, so that enough of y is in
+// flight (two CTAs with y in registers reached 2.9 TB/s in the expand). All
+// barrier waits are bounded; after a timeout the CTA runs on without waiting, so that its
+// cluster's barriers are met.
 #pragma once
 
 #include <cuda.h>
@@ -32,27 +34,28 @@ namespace ck {
 namespace lora {
 
 constexpr int kTcTokens = 128;
-constexpr int kTcWarps = 10;
-constexpr int kTcThreads = 32 * kTcWarps;
+constexpr int kWork = 16;                      // warps that move x, y and out
+constexpr int kTcThreads = 32 * (kWork + 2);
 constexpr int kOp = 128 * 128;                 // bytes of a 128 x 64 operand block, 128-byte swizzle
 constexpr int kTcCols = 256;                   // TMEM columns
-constexpr int kStaging = 32 * 33 * 4;          // a warp's 32 x 32 floats, rows one bank apart
+constexpr int kYRow = 80;                      // a warp's rows of y: 64 bytes, 80 apart (fragment reads hit each bank once)
+constexpr int kYWarp = 32 * kYRow;
+constexpr int kYStage = kWork * kYWarp;
 
 // RB blocks of 64 ranks.
 template <int RB>
 struct LoraTc {
   static constexpr int kStageA = RB * 64 * 128;                        // A: up to 64 RB rows
   static constexpr int kStage = kOp + kStageA;
-  static constexpr int kStages = 4;
-  static constexpr int kPart = (128 * (64 * RB + 4) * 4 + 1023) / 1024 * 1024;   // partial v; then the warps' staging
+  static constexpr int kPart = (128 * (64 * RB + 4) * 4 + 1023) / 1024 * 1024;   // partial v
   static constexpr int kV = kPart;                                     // offset of v: [RB][hi, lo]
   static constexpr int kB = kV + RB * 2 * kOp;                         // offset of B's ring
-  static constexpr int kStagesB = 2;
-  static constexpr int kArea = kB + kStagesB * RB * kOp;
-  static_assert(kArea >= kStages * kStage, "the shrink's stages lie in the same area");
-  static_assert(kPart >= 8 * kStaging, "the staging lies in the partial sums' place");
-  static constexpr int kSmem = 1024 + kArea;
-  static constexpr int kCtas = kSmem <= 112 * 1024 ? 2 : 1;
+  static constexpr int kStagesB = RB == 1 ? 2 : 1;
+  static constexpr int kY = kB + kStagesB * RB * kOp;                  // offset of y's ring
+  static constexpr int kStagesY = RB == 1 ? 3 : 1;
+  static constexpr int kArea = kY + kStagesY * kYStage;
+  static constexpr int kStages = 6;
+  static constexpr int kSmem = 1024 + (kArea > kStages * kStage ? kArea : kStages * kStage);
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16) {
@@ -87,8 +90,20 @@ __device__ __forceinline__ void st_cluster_b32x4(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+// 16 TMEM lanes x 32 columns as MMA accumulator fragments: r[4 j ..] holds columns 8 j + 2 (lane % 4)
+// and + 1 of row lane / 4, then of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 template <typename T, typename TY, int RB>
-__global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
+__global__ void __launch_bounds__(kTcThreads, 1)
     lora_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Params p) {
   using C = LoraTc<RB>;
   using Tr = awq::Traits<T>;
@@ -105,14 +120,14 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
   const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
   volatile int* abort = &abort_flag;
 
-  if (warp == 9) {
+  if (warp == kWork + 1) {
     tmem_alloc(&tmem_base, kTcCols);
     tmem_relinquish();
-  } else if (tid == 8 * 32) {
+  } else if (tid == 32 * kWork) {
     prefetch_tmap(&map_a);
     prefetch_tmap(&map_b);
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 8 * 32 + 1);
+      mbar_init(&full[s], 32 * kWork + 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&shrunk, 1);
@@ -122,7 +137,7 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&dfull[s], 1);
-      mbar_init(&dempty[s], 8);
+      mbar_init(&dempty[s], kWork);
     }
     abort_flag = 0;
     fence_mbarrier_init();
@@ -143,9 +158,9 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
   const int b0 = blocks * rank / ranks, b1 = blocks * (rank + 1) / ranks;
 
   if (n == 0 || adapter < 0) {                                          // the same for the whole cluster
-    if (n > 0) copy_rows(y, out, p, token, n, 128 * b0, min(128 * b1, p.N), warp, kTcWarps, lane);
+    if (n > 0) copy_rows(y, out, p, token, n, 128 * b0, min(128 * b1, p.N), warp, kWork + 2, lane);
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tmem, kTcCols);
+    if (warp == kWork + 1) tmem_dealloc(tmem, kTcCols);
     return;
   }
 
@@ -155,13 +170,13 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
   const int steps = npad / 16;                                          // the expand's K steps
 
   // ------------------------------------------------------------- shrink
-  if (warp < 8) {
-    const int c = tid & 7, r0 = tid >> 3;                               // 16-byte chunk, rows r0 + 32 i
-    const T* src[4];
-    uint32_t dst[4];
+  if (warp < kWork) {
+    const int c = tid & 7, r0 = tid >> 3;                               // 16-byte chunk, rows r0 and r0 + 64
+    const T* src[2];
+    uint32_t dst[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 32 * i;
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 64 * i;
       src[i] = r < n ? x + token[r] * p.ldx + 8 * c : nullptr;
       dst[i] = smem_u32(area) + r * 128 + ((c ^ (r & 7)) << 4);
     }
@@ -175,7 +190,7 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
       mbar_wait(&empty[s], ((i / C::kStages) & 1) ^ 1, abort, 60);
       const bool in = 64 * kb + 8 * c < p.K;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 2; ++j)
         cp_async_16(dst[j] + s * C::kStage, in && src[j] != nullptr ? src[j] + 64 * (int64_t)kb : x, in && src[j] != nullptr);
       cp_async_commit();
       if (i >= kLag) {
@@ -185,7 +200,7 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
     }
     cp_async_wait<0>();
     for (int i = max(k1 - k0 - kLag, 0); i < k1 - k0; ++i) hand_over(i % C::kStages);
-  } else if (warp == 8) {
+  } else if (warp == kWork) {
     if (lane == 0) {
       int issued = 0;
       for (int kb = k0; kb < k1; ++kb, ++issued) {
@@ -225,14 +240,37 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
       tma_load_2d(area + C::kB + (s * RB + rb) * kOp, &map_b, &bfull[s], 64 * rb, adapter * p.N + 128 * (b0 + i));
   };
   const int nb = b1 - b0;
-  if (warp == 8 && lane == 0)
+  if (warp == kWork && lane == 0)
     for (int i = 0; i < min(nb, C::kStagesB); ++i) fetch_b(i);
   __syncwarp();
-  const int q = warp & 3, hc = warp >> 2;                               // TMEM lane quarter, half of the columns
-  if (warp < 8) {
+  // A work warp's piece of an output block: rows 32 q .. of the tile (its TMEM lanes), columns 32 cq ..
+  const int q = warp & 3, cq = warp >> 2;
+  uint8_t* ybuf = area + C::kY + warp * kYWarp;
+  // Block i of y into its ring stage: 4 lanes a row, 8 rows at a time (whole 16 bytes; else element by element).
+  auto fetch_y = [&](int i) {
+    uint8_t* to = ybuf + (i % C::kStagesY) * kYStage;
+    const int c0 = 128 * (b0 + i) + 32 * cq;
+    if (p.vec) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 8 * j + (lane >> 2), col = c0 + 8 * (lane & 3);
+        const bool in = 32 * q + r < n && col < p.N;
+        cp_async_16(smem_u32(to + r * kYRow + 16 * (lane & 3)), in ? y + token[32 * q + r] * p.ldy + col : y, in);
+      }
+    } else if (c0 + lane < p.N) {
+      for (int r = 0; r < 32 && 32 * q + r < n; ++r)
+        reinterpret_cast<TY*>(to + r * kYRow)[lane] = y[token[32 * q + r] * p.ldy + c0 + lane];
+    }
+  };
+  if (warp < kWork) {
+#pragma unroll
+    for (int i = 0; i < C::kStagesY; ++i) {
+      if (i < nb) fetch_y(i);
+      cp_async_commit();                                                // a group a block, empty ones too
+    }
     tc_fence_after();
     float* part = reinterpret_cast<float*>(area) + (32 * q + lane) * (p.R + 4);
-    for (int c0 = 16 * hc; c0 < p.R; c0 += 32) {
+    for (int c0 = 16 * cq; c0 < p.R; c0 += 64) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * q) << 16) + c0, v);
       tmem_ld_wait();
@@ -248,20 +286,29 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
   }
   cluster_sync();
   // half a warp sums a row over the ranks, 8 entries a lane, and hands hi and lo to every CTA
-  if (warp < 8) {
+  if (warp < kWork) {
     const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
     const int l = lane & 15, rows = kTcTokens / ranks;
-    for (int i = 2 * warp + (lane >> 4); i < (rows + 15) / 16 * 16; i += 16) {   // whole warps, for the shuffles
+    for (int i = 2 * warp + (lane >> 4); i < (rows + 31) / 32 * 32; i += 2 * kWork) {   // whole warps, for the shuffles
       const int r = rank * rows + i;
       const bool mine = i < rows;
       float v[8] = {};
-      if (mine && 8 * l < p.R)
-        for (int k = 0; k < ranks; ++k) {
-          const uint32_t at = mapa_shared(smem_u32(area) + (r * (p.R + 4) + 8 * l) * 4, k);
-          const float4 a = ld_cluster_f32x4(at), b = ld_cluster_f32x4(at + 16);
-          v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-          v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-        }
+      if (mine && 8 * l < p.R) {
+        const uint32_t at = smem_u32(area) + (r * (p.R + 4) + 8 * l) * 4;
+        float4 a[8], b[8];                                              // all ranks' loads before the first use
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ranks) {
+            a[k] = ld_cluster_f32x4(mapa_shared(at, k));
+            b[k] = ld_cluster_f32x4(mapa_shared(at, k) + 16);
+          }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ranks) {
+            v[0] += a[k].x, v[1] += a[k].y, v[2] += a[k].z, v[3] += a[k].w;
+            v[4] += b[k].x, v[5] += b[k].y, v[6] += b[k].z, v[7] += b[k].w;
+          }
+      }
       int ex = 0;
       if constexpr (Half2Of<T>::kScaled) {
         uint32_t top = 0;
@@ -292,78 +339,55 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
   fence_proxy_async_any();
 
   // ------------------------------------------------------------- expand
-  if (warp < 8) {
-    float* stage = reinterpret_cast<float*>(area + warp * kStaging);
-    const int rr = 32 * q + (lane >> 2), cc = 8 * (lane & 3);           // rows rr + 8 i of the tile, column of the chunk
-    const TY* yr[4];
-    TY* orow[4];
-    float f[4];
+  if (warp < kWork) {
+    const int g = lane >> 2, t = lane & 3;
+    float f[4];                                                         // scales of rows g + 8 k
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = rr + 8 * i;
-      yr[i] = r < n ? y + token[r] * p.ldy : nullptr;
-      orow[i] = r < n ? out + token[r] * p.ldo : nullptr;
-      f[i] = row_scale[r];
-    }
-    auto load_y = [&](int col, uint4 (&v)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (yr[i] == nullptr || col >= p.N) continue;
-        if (p.vec) {
-          v[i] = *reinterpret_cast<const uint4*>(yr[i] + col);
-        } else {
-          TY e[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = yr[i][min(col + j, p.N - 1)];
-          v[i] = *reinterpret_cast<const uint4*>(e);
-        }
-      }
-    };
-    uint4 yv[4], yn[4];
-    if (nb > 0) load_y(128 * b0 + 64 * hc + cc, yv);
+    for (int k = 0; k < 4; ++k) f[k] = row_scale[32 * q + g + 8 * k];
     for (int i = 0; i < nb; ++i) {
+      uint8_t* yb = ybuf + (i % C::kStagesY) * kYStage;
+      const int c0 = 128 * (b0 + i) + 32 * cq;
+      cp_async_wait<C::kStagesY - 1>();                                 // block i of y is here
       mbar_wait(&dfull[i & 1], (i >> 1) & 1, abort, 65);
       __syncwarp();
       tc_fence_after();
+      uint32_t d[2][16];
+      const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + 128 * (i & 1) + 32 * cq;
+      tmem_ld_16x256b_x4(ta, d[0]);
+      tmem_ld_16x256b_x4(ta + (16u << 16), d[1]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty[i & 1]);
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        const int col = 128 * (b0 + i) + 64 * hc + 32 * ch + cc;
-        // the next chunk's y, while this one is finished
-        load_y(ch == 0 ? col + 32 : i + 1 < nb ? col + 96 : p.N, yn);
-        uint32_t d[32];
-        tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + 128 * (i & 1) + 64 * hc + 32 * ch, d);
-        tmem_ld_wait();
-        if (ch == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&dempty[i & 1]);
+      for (int k = 0; k < 4; ++k)                                       // rows g + 8 k, columns 8 j + 2 t
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          TY* e = reinterpret_cast<TY*>(yb + (g + 8 * k) * kYRow) + 8 * j + 2 * t;
+          uint32_t u = *reinterpret_cast<const uint32_t*>(e);
+          TY* v = reinterpret_cast<TY*>(&u);
+          v[0] = TrY::fromf(fmaf(f[k], __uint_as_float(d[k >> 1][4 * j + 2 * (k & 1)]), TrY::tof(v[0])));
+          v[1] = TrY::fromf(fmaf(f[k], __uint_as_float(d[k >> 1][4 * j + 2 * (k & 1) + 1]), TrY::tof(v[1])));
+          *reinterpret_cast<uint32_t*>(e) = u;
         }
+      __syncwarp();
+      if (p.vec) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = __uint_as_float(d[j]);
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float* s = stage + ((lane >> 2) + 8 * k) * 33 + cc;
-          if (orow[k] != nullptr && col < p.N) {
-            TY e[8];
-            *reinterpret_cast<uint4*>(e) = yv[k];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = TrY::fromf(fmaf(f[k], s[j], TrY::tof(e[j])));
-            if (p.vec) {
-              *reinterpret_cast<uint4*>(orow[k] + col) = *reinterpret_cast<const uint4*>(e);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (col + j < p.N) orow[k][col + j] = e[j];
-            }
-          }
-          yv[k] = yn[k];
+        for (int j = 0; j < 4; ++j) {
+          const int r = 8 * j + g, col = c0 + 8 * t;
+          if (32 * q + r < n && col < p.N)
+            *reinterpret_cast<uint4*>(out + token[32 * q + r] * p.ldo + col) =
+                *reinterpret_cast<const uint4*>(yb + r * kYRow + 16 * t);
         }
-        __syncwarp();
+      } else if (c0 + lane < p.N) {
+        for (int r = 0; r < 32 && 32 * q + r < n; ++r)
+          out[token[32 * q + r] * p.ldo + c0 + lane] = reinterpret_cast<const TY*>(yb + r * kYRow)[lane];
       }
+      __syncwarp();                                                     // the stage is free
+      if (i + C::kStagesY < nb) fetch_y(i + C::kStagesY);
+      cp_async_commit();
     }
-  } else if (warp == 8) {
+  } else if (warp == kWork) {
     if (lane == 0) {
       int issued = min(nb, C::kStagesB);
       for (; issued < nb; ++issued) {
@@ -393,7 +417,7 @@ __global__ void __launch_bounds__(kTcThreads, LoraTc<RB>::kCtas)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kWork + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTcCols);
   }
