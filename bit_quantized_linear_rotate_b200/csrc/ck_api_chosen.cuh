@@ -253,11 +253,17 @@ cudaError_t launch_lora_tc(const ck::lora::Params& p, int64_t tiles, cudaStream_
   if (e != cudaSuccess) return e;
   const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUtensorMap a, b;   // A in boxes of 64 k x R (rounded up) rows, B in boxes of 64 ranks x 128 rows
-  if (make_tmap(&a, p.a, (uint64_t)p.K, (uint64_t)p.L * p.R, (uint64_t)p.K * 2, 64, (uint32_t)((p.R + 15) / 16 * 16),
-                CU_TENSOR_MAP_SWIZZLE_128B, dt) != CK_OK ||
-      make_tmap(&b, p.b, (uint64_t)p.R, (uint64_t)p.L * p.N, (uint64_t)p.R * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B,
-                dt) != CK_OK)
+  const CUtensorMapDataType dy = std::is_same<TY, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  TcMaps m;           // boxes of 64 columns x: A's R rows (rounded up), 128 rows of B, x, y and out
+  if (make_tmap(&m.a, p.a, p.K, (uint64_t)p.L * p.R, (uint64_t)p.K * 2, 64, (uint32_t)((p.R + 15) / 16 * 16), sw, dt) ||
+      make_tmap(&m.b, p.b, p.R, (uint64_t)p.L * p.N, (uint64_t)p.R * 2, 64, 128, sw, dt) ||
+      make_tmap(&m.x, p.x, p.K, p.M, (uint64_t)p.ldx * 2, 64, 128, sw, dt))
+    return cudaErrorInvalidValue;
+  m.y = m.out = m.x;  // not used unless p.vec
+  if (p.vec && (make_tmap(&m.y, p.y, p.N, p.M, (uint64_t)p.ldy * 2, 64, 128, sw, dy) ||
+                make_tmap(&m.out, p.out, p.N, p.M, (uint64_t)p.ldo * 2, 64, 128, sw, dy)))
     return cudaErrorInvalidValue;
   // The cluster size by the time it is expected to take: rounds of one CTA an SM, each 1 / cs of a tile's
   // bytes (at an SM's 43 GB/s) and 6 us for the stages that wait for one another; the number of
@@ -266,11 +272,11 @@ cudaError_t launch_lora_tc(const ck::lora::Params& p, int64_t tiles, cudaStream_
   const double likely = (double)p.M / kTcTokens + std::min<double>(p.L + 1, (double)p.M / kTcTokens) / 2;
   int cs = 1;
   double best = 1e30;
-  for (int c = 1; c <= 8; c *= 2) {
+  for (int c = 1; c <= 8; ++c) {
     const double t = std::ceil(likely * c / sm_count()) * (work / c + fixed);
     if (t < best) best = t, cs = c;
   }
-  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kTcThreads, C::kSmem, st, a, b, p);
+  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kTcThreads, C::kSmem, st, m, p);
 }
 
 template <typename T, typename TY>
@@ -286,6 +292,12 @@ cudaError_t launch_lora(const ck::lora::Params& p, int tm, int64_t tiles, cudaSt
 // Tokens of a tile, by how many tokens an adapter has on average.
 int lora_tile(int64_t M, int64_t L) {
   return M > ck::lora::kSelfGroup && M >= 32 * L ? ck::lora::kTcTokens : 16;
+}
+
+// Whether the CTAs find their tiles themselves; else group_kernel lists them.
+bool lora_finds_tiles(int64_t M, int64_t L) {
+  using namespace ck::lora;
+  return M <= (lora_tile(M, L) == kTcTokens ? kPickTokens : kSelfGroup);
 }
 
 }  // namespace
@@ -356,7 +368,7 @@ ck_status ck_moe_experts_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_
 }
 
 size_t ck_lora_add_workspace_bytes(int64_t M, int64_t L) {
-  if (M <= ck::lora::kSelfGroup || L <= 0) return 0;
+  if (M <= 0 || L <= 0 || lora_finds_tiles(M, L)) return 0;
   return (size_t)ck::lora::max_tiles(M, L, lora_tile(M, L)) * 16 + (size_t)M * 4;   // tile list, token order
 }
 
@@ -401,7 +413,7 @@ ck_status ck_lora_add(const void* y, ck_dtype yt, const void* x, ck_dtype xt, in
   p.tiles = nullptr;
   p.order = nullptr;
   cudaError_t e = cudaSuccess;
-  if (M > kSelfGroup) {
+  if (!lora_finds_tiles(M, L)) {
     const size_t need = ck_lora_add_workspace_bytes(M, L);
     if (!workspace) return fail(CK_ERR_INVALID_ARG, "%s: null workspace", who);
     if (!aligned(workspace, 256)) return fail(CK_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);

@@ -67,33 +67,38 @@ __host__ __device__ inline int64_t max_tiles(int64_t M, int64_t L, int tm) {
 // runs of one id, so a warp mostly counts 256 tokens with one atomic.
 constexpr int kGroupEach = 8;
 
-// The buckets of tokens i0 .. i0 + 7; -1 past the last.
-__device__ __forceinline__ void load_buckets(const int32_t* ids, int64_t i0, int M, int L, int (&a)[kGroupEach]) {
-  const bool wide = (reinterpret_cast<uintptr_t>(ids) & 15) == 0 && i0 + kGroupEach <= M;
-  if (wide) {
-    const int4 v = *reinterpret_cast<const int4*>(ids + i0), w = *reinterpret_cast<const int4*>(ids + i0 + 4);
-    a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w, a[4] = w.x, a[5] = w.y, a[6] = w.z, a[7] = w.w;
-  } else {
+// The buckets of tokens i0 .. i0 + E - 1; -1 past the last.
+template <int E>
+__device__ __forceinline__ void load_buckets(const int32_t* ids, int64_t i0, int M, int L, int (&a)[E]) {
+  const bool wide = (reinterpret_cast<uintptr_t>(ids) & 15) == 0 && i0 + E <= M;
 #pragma unroll
-    for (int j = 0; j < kGroupEach; ++j) a[j] = i0 + j < M ? ids[i0 + j] : 0;
+  for (int j = 0; j < E; j += 4) {
+    if (wide) {
+      const int4 v = *reinterpret_cast<const int4*>(ids + i0 + j);
+      a[j] = v.x, a[j + 1] = v.y, a[j + 2] = v.z, a[j + 3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = j; i < j + 4; ++i) a[i] = i0 + i < M ? ids[i0 + i] : 0;
+    }
   }
 #pragma unroll
-  for (int j = 0; j < kGroupEach; ++j) a[j] = i0 + j >= M ? -1 : a[j] >= 0 && a[j] < L ? a[j] : L;
+  for (int j = 0; j < E; ++j) a[j] = i0 + j >= M ? -1 : a[j] >= 0 && a[j] < L ? a[j] : L;
 }
 
 // Adds each token to its bucket's counter; at[j]: the counter before token j (by a whole warp).
-__device__ __forceinline__ void take_places(int* count, const int (&a)[kGroupEach], int (&at)[kGroupEach]) {
+template <int E>
+__device__ __forceinline__ void take_places(int* count, const int (&a)[E], int (&at)[E]) {
   const int lane = threadIdx.x & 31;
   bool one = a[0] >= 0;
 #pragma unroll
-  for (int j = 1; j < kGroupEach; ++j) one = one && a[j] == a[0];
+  for (int j = 1; j < E; ++j) one = one && a[j] == a[0];
   const unsigned same = __match_any_sync(0xffffffffu, one ? a[0] : -1 - lane);
   const int leader = __ffs(same) - 1;
   int base = 0;
-  if (one && lane == leader) base = atomicAdd(&count[a[0]], kGroupEach * __popc(same));
-  base = __shfl_sync(0xffffffffu, base, leader) + kGroupEach * __popc(same & ((1u << lane) - 1));
+  if (one && lane == leader) base = atomicAdd(&count[a[0]], E * __popc(same));
+  base = __shfl_sync(0xffffffffu, base, leader) + E * __popc(same & ((1u << lane) - 1));
 #pragma unroll
-  for (int j = 0; j < kGroupEach; ++j) at[j] = one ? base + j : a[j] >= 0 ? atomicAdd(&count[a[j]], 1) : 0;
+  for (int j = 0; j < E; ++j) at[j] = one ? base + j : a[j] >= 0 ? atomicAdd(&count[a[j]], 1) : 0;
 }
 
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __restrict__ ids, int M, int L, int tm,
@@ -151,6 +156,98 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
 #pragma unroll
     for (int j = 0; j < kGroupEach; ++j)
       if (a[j] >= 0) order[at[j]] = (int)i0 + j;
+  }
+}
+
+// Tile number `tile` of a batch in one CTA: its adapter (-1: none), its tokens in ascending
+// order and their number (0: there is no such tile). Tiles are numbered by adapter, the tokens
+// without one last. The counts do not depend on the order of the atomics, and only the
+// bucket that holds the tile is ranked, so all CTAs of a cluster find the same. Reading all ids in
+// every CTA costs 2 us at M = 8192, a launch of group_kernel before it 5.
+constexpr int kPickTokens = 32768;     // at most; larger batches use group_kernel
+constexpr int kPickAdapters = kPickTokens / 32;
+constexpr int kPickBytes = (kPickAdapters + 1 + 32 + 8) * 4;
+template <int THREADS, int TM>
+__device__ __forceinline__ void pick_tile(const Params& p, int tile, int* token, int& adapter, int& n, int* scratch) {
+  constexpr int E = 16;                              // ids a thread and round
+  static_assert(THREADS <= 1024, "a warp sums the warps");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = THREADS / 32;
+  int* sums = scratch;                               // [32]
+  int* found = scratch + 32;                         // bucket, its first tile
+  int* count = scratch + 40;                         // [L + 1]
+  for (int i = tid; i <= p.L; i += THREADS) count[i] = 0;
+  if (tid == 0) found[0] = -1;
+  int a[E], at[E];
+  load_buckets(p.ids, E * tid, p.M, p.L, a);
+  __syncthreads();
+  constexpr int kRound = THREADS * E;
+  const int rounds = (p.M + kRound - 1) / kRound;
+  for (int r = 0; r < rounds; ++r) {
+    if (r > 0) load_buckets(p.ids, kRound * r + E * tid, p.M, p.L, a);
+    take_places(count, a, at);
+  }
+  __syncthreads();
+  int before = 0;                                    // tiles of the buckets of earlier rounds
+  for (int b0 = 0; b0 <= p.L; b0 += THREADS) {
+    const int b = b0 + tid;
+    const int nt = b <= p.L ? (count[b] + TM - 1) / TM : 0;
+    int it = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, it, o);
+      if (lane >= o) it += u;
+    }
+    if (lane == 31) sums[warp] = it;
+    __syncthreads();
+    int w = lane < warps ? sums[lane] : 0;           // the warps' totals, as running sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    const int mine = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    const int last = before + (warp > 0 ? mine : 0) + it;
+    if (tile >= last - nt && tile < last) found[0] = b, found[1] = last - nt;
+    before += __shfl_sync(0xffffffffu, w, 31);
+    __syncthreads();
+  }
+  const int bucket = found[0];
+  adapter = bucket < p.L ? bucket : -1;
+  n = 0;
+  if (bucket < 0) return;                            // (adapter is -1, n is 0)
+  const int first = (tile - found[1]) * TM;          // rank of the tile's first token in the bucket
+  n = min(TM, count[bucket] - first);
+  int rank0 = 0;                                     // tokens of the bucket in earlier rounds
+  for (int r = 0; r < rounds; ++r) {
+    const int i0 = kRound * r + E * tid;
+    if (rounds > 1) load_buckets(p.ids, i0, p.M, p.L, a);
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < E; ++j) c += a[j] == bucket;
+    int in = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += u;
+    }
+    if (lane == 31) sums[warp] = in;
+    __syncthreads();
+    int w = lane < warps ? sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    const int mine = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    int at0 = rank0 + (warp > 0 ? mine : 0) + in - c - first;
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (a[j] == bucket) {
+        if (at0 >= 0 && at0 < TM) token[at0] = i0 + j;
+        ++at0;
+      }
+    rank0 += __shfl_sync(0xffffffffu, w, 31);
+    __syncthreads();
   }
 }
 

@@ -14,16 +14,21 @@
 // units to x, y and out; with mma.sync fragments straight from global
 // memory the M = 8192, R = 64 case took 190 us.
 //
-// Warps 0-15 bring x in (16-byte asynchronous copies: a tile's tokens may be any rows), later
-// reduce v, bring in y and write the output; warp 16 brings in A and B by tensor copies
-// (rows of another adapter and zeros past the end fill what R leaves of a block); warp 17
-// issues the MMAs.
+// Prompts are mostly tiles of consecutive tokens: then x and y come by tensor copies, and a full
+// tile's output leaves by tensor stores. Any other tile is moved by 16-byte asynchronous
+// copies and stores of the work warps (a quarter of an SM's load-store time for each 128 x 128 block
+// of output goes to y, another to the output: such tiles run at half the rate), or element by
+// element where y's rows do not start on 16 bytes.
+//
+// Warps 0-15 move x of such tiles, later reduce v and finish the output; warp 16 brings in A, B
+// and x by tensor copies (rows of another adapter and zeros past the end fill what R leaves of a
+// block); warp 17 issues the MMAs; warp 18 brings in y and stores the output. (y by bulk copies of
+// one row's 256 bytes was slowest of all: 62 us where 25 had been.)
 //
 // Shared memory, one area used twice (LoraTc): the shrink's stages, then the partial sums of v,
-// v as operands, the ring of B and the ring of y. One CTA an SM, so that enough of y is in
-// flight (two CTAs with y in registers reached 2.9 TB/s in the expand). All
-// barrier waits are bounded; after a timeout the CTA runs on without waiting, so that its
-// cluster's barriers are met.
+// v as operands, the ring of B and the ring of y, where the output forms in place. One CTA
+// an SM. All barrier waits are bounded; after a timeout the CTA runs on without waiting,
+// so that its cluster's barriers are met.
 #pragma once
 
 #include <cuda.h>
@@ -35,12 +40,13 @@ namespace lora {
 
 constexpr int kTcTokens = 128;
 constexpr int kWork = 16;                      // warps that move x, y and out
-constexpr int kTcThreads = 32 * (kWork + 2);
+constexpr int kTcThreads = 32 * (kWork + 3);
 constexpr int kOp = 128 * 128;                 // bytes of a 128 x 64 operand block, 128-byte swizzle
 constexpr int kTcCols = 256;                   // TMEM columns
-constexpr int kYRow = 80;                      // a warp's rows of y: 64 bytes, 80 apart (fragment reads hit each bank once)
-constexpr int kYWarp = 32 * kYRow;
-constexpr int kYStage = kWork * kYWarp;
+constexpr int kYStage = 2 * kOp;               // a 128 x 128 block of y: two boxes of 64 columns, 128-byte swizzle
+
+// Offset of row r, 16-byte chunk c (0 .. 15) of a block of y.
+__device__ __forceinline__ int y_at(int r, int c) { return (c >> 3) * kOp + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 
 // RB blocks of 64 ranks.
 template <int RB>
@@ -54,8 +60,9 @@ struct LoraTc {
   static constexpr int kY = kB + kStagesB * RB * kOp;                  // offset of y's ring
   static constexpr int kStagesY = RB == 1 ? 3 : 1;
   static constexpr int kArea = kY + kStagesY * kYStage;
-  static constexpr int kStages = 6;
-  static constexpr int kSmem = 1024 + (kArea > kStages * kStage ? kArea : kStages * kStage);
+  static constexpr int kStages = RB == 1 ? 8 : 5;
+  static constexpr int kSearch = kStages * kStage;                     // offset of the tile search's counters
+  static constexpr int kSmem = 1024 + (kArea > kSearch + kPickBytes ? kArea : kSearch + kPickBytes);
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16) {
@@ -77,7 +84,9 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void fence_proxy_async_any() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
@@ -89,6 +98,23 @@ __device__ __forceinline__ void st_cluster_b32x4(uint32_t addr, uint4 v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
+
+// a: (L R, K), b: (L N, R), x: (M, K), y and out: (M, N); the last two only where p.vec.
+struct TcMaps {
+  CUtensorMap a, b, x, y, out;
+};
+
+__device__ __forceinline__ void tma_store_2d(const void* tmap, const void* smem, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(smem_u32(smem)), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until at most N of this thread's groups still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 16 TMEM lanes x 32 columns as MMA accumulator fragments: r[4 j ..] holds columns 8 j + 2 (lane % 4)
 // and + 1 of row lane / 4, then of row lane / 4 + 8.
@@ -104,7 +130,7 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 
 template <typename T, typename TY, int RB>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    lora_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Params p) {
+    lora_tc_kernel(const __grid_constant__ TcMaps maps, const Params p) {
   using C = LoraTc<RB>;
   using Tr = awq::Traits<T>;
   using TrY = awq::Traits<TY>;
@@ -112,6 +138,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* area = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   __shared__ uint64_t full[C::kStages], empty[C::kStages], shrunk;      // the shrink's stages, its end
   __shared__ uint64_t bfull[C::kStagesB], bempty[C::kStagesB], dfull[2], dempty[2];
+  __shared__ uint64_t yfull[C::kStagesY], ydone[C::kStagesY];
   __shared__ int abort_flag;
   __shared__ uint32_t tmem_base;
   __shared__ int token[kTcTokens];
@@ -124,10 +151,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tmem_alloc(&tmem_base, kTcCols);
     tmem_relinquish();
   } else if (tid == 32 * kWork) {
-    prefetch_tmap(&map_a);
-    prefetch_tmap(&map_b);
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+    prefetch_tmap(&maps.x);
+    abort_flag = 0;
+  }
+  tc_fence_before();
+  grid_dep_wait();
+  grid_dep_launch();
+  int adapter, n;
+  if (p.tiles != nullptr) {
+    const int4 tile = __ldcg(reinterpret_cast<const int4*>(p.tiles) + blockIdx.x / ranks);
+    adapter = tile.x, n = tile.z;
+    if (tid < n) token[tid] = __ldcg(p.order + tile.y + tid);
+  } else {
+    pick_tile<kTcThreads, kTcTokens>(p, (int)(blockIdx.x / ranks), token, adapter, n,
+                                     reinterpret_cast<int*>(area + C::kSearch));
+    fence_proxy_async_smem();                                           // tensor copies may come there later
+  }
+  __syncthreads();
+  // consecutive tokens: x by tensor copies; whole 16-byte pieces too: y as well
+  const bool seq = __syncthreads_and(tid >= n || token[tid] == token[0] + tid) != 0;
+  const bool seq_y = seq && p.vec, dense = seq_y && n == kTcTokens;
+  if (tid == 32 * kWork) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 32 * kWork + 1);
+      mbar_init(&full[s], seq ? 1 : 32 * kWork + 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&shrunk, 1);
@@ -135,19 +183,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&bfull[s], 1);
       mbar_init(&bempty[s], 1);
     }
+    for (int s = 0; s < C::kStagesY; ++s) {
+      mbar_init(&yfull[s], 1);
+      mbar_init(&ydone[s], kWork);
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&dfull[s], 1);
       mbar_init(&dempty[s], kWork);
     }
-    abort_flag = 0;
     fence_mbarrier_init();
   }
-  tc_fence_before();
-  grid_dep_wait();
-  grid_dep_launch();
-  const int4 tile = __ldcg(reinterpret_cast<const int4*>(p.tiles) + blockIdx.x / ranks);
-  const int adapter = tile.x, n = tile.z;
-  if (tid < n) token[tid] = __ldcg(p.order + tile.y + tid);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
@@ -158,7 +203,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int b0 = blocks * rank / ranks, b1 = blocks * (rank + 1) / ranks;
 
   if (n == 0 || adapter < 0) {                                          // the same for the whole cluster
-    if (n > 0) copy_rows(y, out, p, token, n, 128 * b0, min(128 * b1, p.N), warp, kWork + 2, lane);
+    if (n > 0) copy_rows(y, out, p, token, n, 128 * b0, min(128 * b1, p.N), warp, kWork + 3, lane);
     __syncthreads();
     if (warp == kWork + 1) tmem_dealloc(tmem, kTcCols);
     return;
@@ -170,7 +215,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int steps = npad / 16;                                          // the expand's K steps
 
   // ------------------------------------------------------------- shrink
-  if (warp < kWork) {
+  if (warp < kWork && !seq) {
     const int c = tid & 7, r0 = tid >> 3;                               // 16-byte chunk, rows r0 and r0 + 64
     const T* src[2];
     uint32_t dst[2];
@@ -180,7 +225,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       src[i] = r < n ? x + token[r] * p.ldx + 8 * c : nullptr;
       dst[i] = smem_u32(area) + r * 128 + ((c ^ (r & 7)) << 4);
     }
-    constexpr int kLag = C::kStages - 1;
+    // a stage is handed over kLag blocks after its copies began, and free again some blocks later: two
+    // fewer than there are stages, else every block waits for the MMAs of the one just handed over
+    constexpr int kLag = C::kStages - 3;
     auto hand_over = [&](int s) {                                       // this thread's copies into stage s are done
       fence_proxy_async_smem();
       mbar_arrive(&full[s]);
@@ -206,14 +253,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int kb = k0; kb < k1; ++kb, ++issued) {
         const int i = kb - k0, s = i % C::kStages;
         if (!mbar_wait(&empty[s], ((i / C::kStages) & 1) ^ 1, abort, 61)) break;
-        mbar_arrive_expect_tx(&full[s], npad * 128);
-        tma_load_2d(area + s * C::kStage + kOp, &map_a, &full[s], 64 * kb, adapter * p.R);
+        mbar_arrive_expect_tx(&full[s], npad * 128 + (seq ? kOp : 0));
+        if (seq) tma_load_2d(area + s * C::kStage, &maps.x, &full[s], 64 * kb, token[0]);   // rows past n: nobody reads them
+        tma_load_2d(area + s * C::kStage + kOp, &maps.a, &full[s], 64 * kb, adapter * p.R);
       }
       if (*abort)
         for (int i = issued - 1; i >= 0 && i >= issued - C::kStages; --i)
           mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, nullptr, 62, 100000000ull);
     }
-  } else if (lane == 0) {
+  } else if (warp == kWork + 1 && lane == 0) {
     const uint32_t id = idesc_f16(128, npad, sizeof(T) == 2 && !Half2Of<T>::kScaled);
     for (int kb = k0; kb < k1; ++kb) {
       const int i = kb - k0, s = i % C::kStages;
@@ -237,7 +285,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int s = i % C::kStagesB;
     mbar_arrive_expect_tx(&bfull[s], RB * kOp);
     for (int rb = 0; rb < RB; ++rb)
-      tma_load_2d(area + C::kB + (s * RB + rb) * kOp, &map_b, &bfull[s], 64 * rb, adapter * p.N + 128 * (b0 + i));
+      tma_load_2d(area + C::kB + (s * RB + rb) * kOp, &maps.b, &bfull[s], 64 * rb, adapter * p.N + 128 * (b0 + i));
   };
   const int nb = b1 - b0;
   if (warp == kWork && lane == 0)
@@ -245,29 +293,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncwarp();
   // A work warp's piece of an output block: rows 32 q .. of the tile (its TMEM lanes), columns 32 cq ..
   const int q = warp & 3, cq = warp >> 2;
-  uint8_t* ybuf = area + C::kY + warp * kYWarp;
-  // Block i of y into its ring stage: 4 lanes a row, 8 rows at a time (whole 16 bytes; else element by element).
+  // Block i of y into its ring stage by tensor copies (one thread of warp 18) ...
+  auto copy_y = [&](int i) {
+    const int s = i % C::kStagesY, c0 = 128 * (b0 + i), boxes = c0 + 64 < p.N ? 2 : 1;
+    mbar_arrive_expect_tx(&yfull[s], boxes * kOp);
+    for (int h = 0; h < boxes; ++h)
+      tma_load_2d(area + C::kY + s * kYStage + h * kOp, &maps.y, &yfull[s], c0 + 64 * h, token[0]);
+  };
+  // ... or a work warp's piece of it: 4 lanes a row, 8 rows at a time; rows that do not start on 16 bytes
+  // element by element, a column a lane.
   auto fetch_y = [&](int i) {
-    uint8_t* to = ybuf + (i % C::kStagesY) * kYStage;
+    uint8_t* to = area + C::kY + (i % C::kStagesY) * kYStage;
     const int c0 = 128 * (b0 + i) + 32 * cq;
     if (p.vec) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = 8 * j + (lane >> 2), col = c0 + 8 * (lane & 3);
-        const bool in = 32 * q + r < n && col < p.N;
-        cp_async_16(smem_u32(to + r * kYRow + 16 * (lane & 3)), in ? y + token[32 * q + r] * p.ldy + col : y, in);
+        const int r = 32 * q + 8 * j + (lane >> 2), col = c0 + 8 * (lane & 3);
+        const bool in = r < n && col < p.N;
+        cp_async_16(smem_u32(to + y_at(r, 4 * cq + (lane & 3))), in ? y + token[r] * p.ldy + col : y, in);
       }
     } else if (c0 + lane < p.N) {
-      for (int r = 0; r < 32 && 32 * q + r < n; ++r)
-        reinterpret_cast<TY*>(to + r * kYRow)[lane] = y[token[32 * q + r] * p.ldy + c0 + lane];
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 8) {
+        TY e[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) e[r] = y[token[min(32 * q + r0 + r, n - 1)] * p.ldy + c0 + lane];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          reinterpret_cast<TY*>(to + y_at(32 * q + r0 + r, 4 * cq + (lane >> 3)))[lane & 7] = e[r];
+      }
     }
   };
+  if (warp == kWork + 2 && lane == 0 && seq_y)
+    for (int i = 0; i < min(nb, C::kStagesY); ++i) copy_y(i);
+  __syncwarp();
   if (warp < kWork) {
-#pragma unroll
-    for (int i = 0; i < C::kStagesY; ++i) {
-      if (i < nb) fetch_y(i);
-      cp_async_commit();                                                // a group a block, empty ones too
-    }
     tc_fence_after();
     float* part = reinterpret_cast<float*>(area) + (32 * q + lane) * (p.R + 4);
     for (int c0 = 16 * cq; c0 < p.R; c0 += 64) {
@@ -283,15 +343,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     tc_fence_before();
+    if (!seq_y) {
+      if (nb > 0) fetch_y(0);                                           // while v is exchanged
+      cp_async_commit();                                                // a group a block, empty ones too
+    }
   }
   cluster_sync();
   // half a warp sums a row over the ranks, 8 entries a lane, and hands hi and lo to every CTA
   if (warp < kWork) {
     const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
-    const int l = lane & 15, rows = kTcTokens / ranks;
+    const int l = lane & 15, rows = (kTcTokens + ranks - 1) / ranks;
     for (int i = 2 * warp + (lane >> 4); i < (rows + 31) / 32 * 32; i += 2 * kWork) {   // whole warps, for the shuffles
       const int r = rank * rows + i;
-      const bool mine = i < rows;
+      const bool mine = i < rows && r < kTcTokens;
       float v[8] = {};
       if (mine && 8 * l < p.R) {
         const uint32_t at = smem_u32(area) + (r * (p.R + 4) + 8 * l) * 4;
@@ -333,21 +397,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (mine && l == 0)
         for (int k = 0; k < ranks; ++k) st_cluster_f32(mapa_shared(smem_u32(row_scale) + 4 * r, k), as * exp2_int(-ex));
     }
-    fence_proxy_async_any();                                            // v is read by the tensor cores
+    fence_proxy_async_cluster();                                        // v is read by the tensor cores
   }
   cluster_sync();
-  fence_proxy_async_any();
+  fence_proxy_async_cluster();
 
   // ------------------------------------------------------------- expand
   if (warp < kWork) {
+    if (!seq_y) {
+#pragma unroll
+      for (int i = 1; i < C::kStagesY; ++i) {
+        if (i < nb) fetch_y(i);
+        cp_async_commit();
+      }
+    }
     const int g = lane >> 2, t = lane & 3;
     float f[4];                                                         // scales of rows g + 8 k
 #pragma unroll
     for (int k = 0; k < 4; ++k) f[k] = row_scale[32 * q + g + 8 * k];
     for (int i = 0; i < nb; ++i) {
-      uint8_t* yb = ybuf + (i % C::kStagesY) * kYStage;
+      const int ys = i % C::kStagesY;
+      uint8_t* yb = area + C::kY + ys * kYStage;
       const int c0 = 128 * (b0 + i) + 32 * cq;
-      cp_async_wait<C::kStagesY - 1>();                                 // block i of y is here
+      if (seq_y) mbar_wait(&yfull[ys], (i / C::kStagesY) & 1, abort, 70);
+      else cp_async_wait<C::kStagesY - 1>();                            // block i of y is here
       mbar_wait(&dfull[i & 1], (i >> 1) & 1, abort, 65);
       __syncwarp();
       tc_fence_after();
@@ -363,29 +436,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int k = 0; k < 4; ++k)                                       // rows g + 8 k, columns 8 j + 2 t
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          TY* e = reinterpret_cast<TY*>(yb + (g + 8 * k) * kYRow) + 8 * j + 2 * t;
-          uint32_t u = *reinterpret_cast<const uint32_t*>(e);
+          uint32_t* e = reinterpret_cast<uint32_t*>(yb + y_at(32 * q + g + 8 * k, 4 * cq + j)) + t;
+          uint32_t u = *e;
           TY* v = reinterpret_cast<TY*>(&u);
           v[0] = TrY::fromf(fmaf(f[k], __uint_as_float(d[k >> 1][4 * j + 2 * (k & 1)]), TrY::tof(v[0])));
           v[1] = TrY::fromf(fmaf(f[k], __uint_as_float(d[k >> 1][4 * j + 2 * (k & 1) + 1]), TrY::tof(v[1])));
-          *reinterpret_cast<uint32_t*>(e) = u;
+          *e = u;
         }
-      __syncwarp();
-      if (p.vec) {
+      if (!dense) {
+        __syncwarp();
+        if (p.vec) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 8 * j + g, col = c0 + 8 * t;
-          if (32 * q + r < n && col < p.N)
-            *reinterpret_cast<uint4*>(out + token[32 * q + r] * p.ldo + col) =
-                *reinterpret_cast<const uint4*>(yb + r * kYRow + 16 * t);
+          for (int j = 0; j < 4; ++j) {
+            const int r = 32 * q + 8 * j + g, col = c0 + 8 * t;
+            if (r < n && col < p.N)
+              *reinterpret_cast<uint4*>(out + token[r] * p.ldo + col) =
+                  *reinterpret_cast<const uint4*>(yb + y_at(r, 4 * cq + t));
+          }
+        } else if (c0 + lane < p.N) {
+#pragma unroll 8
+          for (int r = 32 * q; r < 32 * q + 32; ++r)
+            if (r < n)
+              out[token[r] * p.ldo + c0 + lane] =
+                  reinterpret_cast<const TY*>(yb + y_at(r, 4 * cq + (lane >> 3)))[lane & 7];
         }
-      } else if (c0 + lane < p.N) {
-        for (int r = 0; r < 32 && 32 * q + r < n; ++r)
-          out[token[32 * q + r] * p.ldo + c0 + lane] = reinterpret_cast<const TY*>(yb + r * kYRow)[lane];
       }
-      __syncwarp();                                                     // the stage is free
-      if (i + C::kStagesY < nb) fetch_y(i + C::kStagesY);
-      cp_async_commit();
+      if (seq_y) {
+        fence_proxy_async_smem();                                       // a tensor store or copy comes next
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ydone[ys]);
+      } else {
+        __syncwarp();                                                   // the stage is free
+        if (i + C::kStagesY < nb) fetch_y(i + C::kStagesY);
+        cp_async_commit();
+      }
+    }
+  } else if (warp == kWork + 2) {
+    if (lane == 0 && seq_y) {
+      int issued = min(nb, C::kStagesY), i = 0;
+      for (; i < nb; ++i) {
+        const int s = i % C::kStagesY, c0 = 128 * (b0 + i);
+        if (!mbar_wait(&ydone[s], (i / C::kStagesY) & 1, abort, 71)) break;
+        if (dense) {
+          for (int h = 0; h < 2 && c0 + 64 * h < p.N; ++h)
+            tma_store_2d(&maps.out, area + C::kY + s * kYStage + h * kOp, c0 + 64 * h, token[0]);
+          bulk_commit();
+        }
+        // the stage of block i - kBack has been read: fetch into it
+        constexpr int kBack = C::kStagesY > 1 ? 1 : 0;
+        if (dense) bulk_wait_read<kBack>();
+        if (i >= kBack && issued < nb) copy_y(issued++);
+      }
+      bulk_wait_all();
+      if (i < nb)                                                       // gave up: the copies in flight
+        for (int k = issued - 1; k >= 0 && k >= issued - C::kStagesY; --k)
+          mbar_wait(&yfull[k % C::kStagesY], (k / C::kStagesY) & 1, nullptr, 72, 100000000ull);
     }
   } else if (warp == kWork) {
     if (lane == 0) {
@@ -398,7 +503,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = issued - 1; i >= 0 && i >= issued - C::kStagesB; --i)
           mbar_wait(&bfull[i % C::kStagesB], (i / C::kStagesB) & 1, nullptr, 67, 100000000ull);
     }
-  } else if (lane == 0) {
+  } else if (lane == 0) {                                               // warp 17
     const uint32_t id = idesc_f16(128, 128, sizeof(T) == 2 && !Half2Of<T>::kScaled);
     for (int i = 0; i < nb; ++i) {
       const int s = i % C::kStagesB;
