@@ -85,20 +85,44 @@ __device__ __forceinline__ void load_buckets(const int32_t* ids, int64_t i0, int
   for (int j = 0; j < E; ++j) a[j] = i0 + j >= M ? -1 : a[j] >= 0 && a[j] < L ? a[j] : L;
 }
 
-// Adds each token to its bucket's counter; at[j]: the counter before token j (by a whole warp).
+// a[j] without indexing registers by a variable.
+template <int E>
+__device__ __forceinline__ int pick(const int (&a)[E], int j) {
+  int v = a[0];
+#pragma unroll
+  for (int k = 1; k < E; ++k) v = k == j ? a[k] : v;
+  return v;
+}
+
+// Adds each token to its bucket's counter; at[j]: the counter before token j (by a whole warp). One
+// atomic where all the warp's tokens are of one bucket, else one for each run of a thread.
 template <int E>
 __device__ __forceinline__ void take_places(int* count, const int (&a)[E], int (&at)[E]) {
   const int lane = threadIdx.x & 31;
   bool one = a[0] >= 0;
 #pragma unroll
   for (int j = 1; j < E; ++j) one = one && a[j] == a[0];
-  const unsigned same = __match_any_sync(0xffffffffu, one ? a[0] : -1 - lane);
-  const int leader = __ffs(same) - 1;
-  int base = 0;
-  if (one && lane == leader) base = atomicAdd(&count[a[0]], E * __popc(same));
-  base = __shfl_sync(0xffffffffu, base, leader) + E * __popc(same & ((1u << lane) - 1));
+  const int a0 = __shfl_sync(0xffffffffu, a[0], 0);  // (not in a condition that only some lanes evaluate)
+  one = __all_sync(0xffffffffu, one && a[0] == a0);
+  if (one) {
+    int base = 0;
+    if (lane == 0) base = atomicAdd(&count[a[0]], 32 * E);
+    base = __shfl_sync(0xffffffffu, base, 0) + E * lane;
 #pragma unroll
-  for (int j = 0; j < E; ++j) at[j] = one ? base + j : a[j] >= 0 ? atomicAdd(&count[a[j]], 1) : 0;
+    for (int j = 0; j < E; ++j) at[j] = base + j;
+    return;
+  }
+#pragma unroll 1
+  for (int j = 0; j < E;) {
+    int n = 0;                                       // a run from j on
+    const int b = pick(a, j);
+    while (j + n < E && pick(a, j + n) == b) ++n;
+    const int base = b >= 0 ? atomicAdd(&count[b], n) : 0;
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k >= j && k < j + n) at[k] = base + k - j;
+    j += n;
+  }
 }
 
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __restrict__ ids, int M, int L, int tm,
@@ -162,61 +186,52 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
 // Tile number `tile` of a batch in one CTA: its adapter (-1: none), its tokens in ascending
 // order and their number (0: there is no such tile). Tiles are numbered by adapter, the tokens
 // without one last. The counts do not depend on the order of the atomics, and only the
-// bucket that holds the tile is ranked, so all CTAs of a cluster find the same. Reading all ids in
-// every CTA costs 2 us at M = 8192, a launch of group_kernel before it 5.
+// bucket that holds the tile is ranked, so all CTAs of a cluster find the same. `scratch`
+// (kPickBytes) must be zero, before a barrier; token[] may be read after the next one. Reading all
+// ids in every CTA costs less than a launch of group_kernel before it (5 us at M = 8192).
 constexpr int kPickTokens = 32768;     // at most; larger batches use group_kernel
 constexpr int kPickAdapters = kPickTokens / 32;
-constexpr int kPickBytes = (kPickAdapters + 1 + 32 + 8) * 4;
+constexpr int kPickBytes = (kPickAdapters + 1 + 32) * 4;
 template <int THREADS, int TM>
 __device__ __forceinline__ void pick_tile(const Params& p, int tile, int* token, int& adapter, int& n, int* scratch) {
   constexpr int E = 16;                              // ids a thread and round
-  static_assert(THREADS <= 1024, "a warp sums the warps");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = THREADS / 32;
+  constexpr int kRound = THREADS * E, warps = THREADS / 32;
+  static_assert(warps <= 32, "a warp sums the warps");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* sums = scratch;                               // [32]
-  int* found = scratch + 32;                         // bucket, its first tile
-  int* count = scratch + 40;                         // [L + 1]
-  for (int i = tid; i <= p.L; i += THREADS) count[i] = 0;
-  if (tid == 0) found[0] = -1;
+  int* count = scratch + 32;                         // [L + 1]
   int a[E], at[E];
-  load_buckets(p.ids, E * tid, p.M, p.L, a);
-  __syncthreads();
-  constexpr int kRound = THREADS * E;
   const int rounds = (p.M + kRound - 1) / kRound;
   for (int r = 0; r < rounds; ++r) {
-    if (r > 0) load_buckets(p.ids, kRound * r + E * tid, p.M, p.L, a);
-    take_places(count, a, at);
+    load_buckets(p.ids, kRound * r + E * tid, p.M, p.L, a);
+    if (__any_sync(0xffffffffu, a[0] >= 0)) take_places(count, a, at);
   }
   __syncthreads();
-  int before = 0;                                    // tiles of the buckets of earlier rounds
-  for (int b0 = 0; b0 <= p.L; b0 += THREADS) {
-    const int b = b0 + tid;
-    const int nt = b <= p.L ? (count[b] + TM - 1) / TM : 0;
+  // every warp for itself: the bucket that holds the tile
+  int bucket = -1, first = 0, before = 0;
+  for (int b0 = 0; b0 <= p.L && bucket < 0; b0 += 32) {
+    const int c = b0 + lane <= p.L ? count[b0 + lane] : 0, nt = (c + TM - 1) / TM;
     int it = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, it, o);
       if (lane >= o) it += u;
     }
-    if (lane == 31) sums[warp] = it;
-    __syncthreads();
-    int w = lane < warps ? sums[lane] : 0;           // the warps' totals, as running sums
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
+    const int last = before + it;
+    const unsigned here = __ballot_sync(0xffffffffu, tile >= last - nt && tile < last);
+    if (here != 0) {
+      const int l = __ffs(here) - 1;
+      bucket = b0 + l;
+      first = (tile - __shfl_sync(0xffffffffu, last - nt, l)) * TM;   // rank of the tile's first token
+      n = min(TM, __shfl_sync(0xffffffffu, c, l) - first);
     }
-    const int mine = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-    const int last = before + (warp > 0 ? mine : 0) + it;
-    if (tile >= last - nt && tile < last) found[0] = b, found[1] = last - nt;
-    before += __shfl_sync(0xffffffffu, w, 31);
-    __syncthreads();
+    before = __shfl_sync(0xffffffffu, last, 31);
   }
-  const int bucket = found[0];
   adapter = bucket < p.L ? bucket : -1;
-  n = 0;
-  if (bucket < 0) return;                            // (adapter is -1, n is 0)
-  const int first = (tile - found[1]) * TM;          // rank of the tile's first token in the bucket
-  n = min(TM, count[bucket] - first);
+  if (bucket < 0) {
+    n = 0;
+    return;
+  }
   int rank0 = 0;                                     // tokens of the bucket in earlier rounds
   for (int r = 0; r < rounds; ++r) {
     const int i0 = kRound * r + E * tid;
@@ -230,24 +245,20 @@ __device__ __forceinline__ void pick_tile(const Params& p, int tile, int* token,
       const int u = __shfl_up_sync(0xffffffffu, in, o);
       if (lane >= o) in += u;
     }
+    if (r > 0) __syncthreads();                      // sums has been read
     if (lane == 31) sums[warp] = in;
     __syncthreads();
-    int w = lane < warps ? sums[lane] : 0;
+    const int w = lane < warps ? sums[lane] : 0;
+    int at0 = rank0 + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + in - c - first;
+    if (at0 < TM && at0 + c > 0) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
+      for (int j = 0; j < E; ++j)
+        if (a[j] == bucket) {
+          if (at0 >= 0 && at0 < TM) token[at0] = i0 + j;
+          ++at0;
+        }
     }
-    const int mine = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-    int at0 = rank0 + (warp > 0 ? mine : 0) + in - c - first;
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (a[j] == bucket) {
-        if (at0 >= 0 && at0 < TM) token[at0] = i0 + j;
-        ++at0;
-      }
-    rank0 += __shfl_sync(0xffffffffu, w, 31);
-    __syncthreads();
+    rank0 += __reduce_add_sync(0xffffffffu, w);
   }
 }
 
@@ -314,18 +325,31 @@ __device__ __forceinline__ void split(float v, T& hi, T& lo) {
   lo = awq::Traits<T>::fromf(isfinite(h) ? v - h : 0.0f);
 }
 
-// Columns [c0, c1) of y's rows token[0 .. n) into out (nothing where out is y).
+// Columns [c0, c1) of y's rows token[0 .. n) into out (nothing where out is y): a row a warp, eight
+// pieces a lane in flight (c0 % 8 == 0 and c1 % 8 == 0 where p.vec).
 template <typename TY>
 __device__ __forceinline__ void copy_rows(const TY* y, TY* out, const Params& p, const int* token, int n, int c0, int c1,
-                                          int warp, int warps, int lane) {
+                                          int warp, int warps) {
   if (y == out) return;
+  const int lane = threadIdx.x & 31, per = p.vec ? (c1 - c0) / 8 : c1 - c0;   // pieces a row
   for (int m = warp; m < n; m += warps) {
-    const TY* yp = y + token[m] * p.ldy;
-    TY* op = out + token[m] * p.ldo;
-    if (p.vec)
-      for (int c = c0 + 8 * lane; c < c1; c += 256) *reinterpret_cast<uint4*>(op + c) = *reinterpret_cast<const uint4*>(yp + c);
-    else
-      for (int c = c0 + lane; c < c1; c += 32) op[c] = yp[c];
+    const TY* from = y + token[m] * p.ldy + c0;
+    TY* to = out + token[m] * p.ldo + c0;
+    for (int k = lane; k < per; k += 256) {
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k + 32 * j < per) {
+          if (p.vec) v[j] = reinterpret_cast<const uint4*>(from)[k + 32 * j];
+          else v[j].x = reinterpret_cast<const uint16_t*>(from)[k + 32 * j];
+        }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k + 32 * j < per) {
+          if (p.vec) reinterpret_cast<uint4*>(to)[k + 32 * j] = v[j];
+          else reinterpret_cast<uint16_t*>(to)[k + 32 * j] = (uint16_t)v[j].x;
+        }
+    }
   }
 }
 
@@ -365,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
   const int nb0 = (int)((int64_t)nb * rank / ranks), nb1 = (int)((int64_t)nb * (rank + 1) / ranks);
 
   if (adapter < 0) {                                  // tokens without an adapter
-    copy_rows(y, out, p, S.token, n, 32 * nb0, min(32 * nb1, p.N), warp, kWarps, lane);
+    copy_rows(y, out, p, S.token, n, 32 * nb0, min(32 * nb1, p.N), warp, kWarps);
     return;
   }
 

@@ -84,9 +84,9 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void fence_proxy_async_cluster() {
-  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
-}
+// The halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
@@ -94,11 +94,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_cluster_b32x4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
 // a: (L R, K), b: (L N, R), x: (M, K), y and out: (M, N); the last two only where p.vec.
 struct TcMaps {
   CUtensorMap a, b, x, y, out;
@@ -136,7 +131,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using TrY = awq::Traits<TY>;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* area = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  __shared__ uint64_t full[C::kStages], empty[C::kStages], shrunk;      // the shrink's stages, its end
+  // the shrink's stages (filled by tensor copies, or with the work warps' help), and its end
+  __shared__ uint64_t full1[C::kStages], full2[C::kStages], empty[C::kStages], shrunk;
   __shared__ uint64_t bfull[C::kStagesB], bempty[C::kStagesB], dfull[2], dempty[2];
   __shared__ uint64_t yfull[C::kStagesY], ydone[C::kStagesY];
   __shared__ int abort_flag;
@@ -154,28 +150,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefetch_tmap(&maps.a);
     prefetch_tmap(&maps.b);
     prefetch_tmap(&maps.x);
-    abort_flag = 0;
-  }
-  tc_fence_before();
-  grid_dep_wait();
-  grid_dep_launch();
-  int adapter, n;
-  if (p.tiles != nullptr) {
-    const int4 tile = __ldcg(reinterpret_cast<const int4*>(p.tiles) + blockIdx.x / ranks);
-    adapter = tile.x, n = tile.z;
-    if (tid < n) token[tid] = __ldcg(p.order + tile.y + tid);
-  } else {
-    pick_tile<kTcThreads, kTcTokens>(p, (int)(blockIdx.x / ranks), token, adapter, n,
-                                     reinterpret_cast<int*>(area + C::kSearch));
-    fence_proxy_async_smem();                                           // tensor copies may come there later
-  }
-  __syncthreads();
-  // consecutive tokens: x by tensor copies; whole 16-byte pieces too: y as well
-  const bool seq = __syncthreads_and(tid >= n || token[tid] == token[0] + tid) != 0;
-  const bool seq_y = seq && p.vec, dense = seq_y && n == kTcTokens;
-  if (tid == 32 * kWork) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], seq ? 1 : 32 * kWork + 1);
+      mbar_init(&full1[s], 1);
+      mbar_init(&full2[s], 32 * kWork + 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&shrunk, 1);
@@ -191,9 +168,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&dfull[s], 1);
       mbar_init(&dempty[s], kWork);
     }
+    abort_flag = 0;
     fence_mbarrier_init();
   }
+  int* search = reinterpret_cast<int*>(area + C::kSearch);
+  for (int i = tid; i < kPickBytes / 4; i += kTcThreads) search[i] = 0;
+  tc_fence_before();
   __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+  int adapter, n;
+  if (p.tiles != nullptr) {
+    const int4 tile = __ldcg(reinterpret_cast<const int4*>(p.tiles) + blockIdx.x / ranks);
+    adapter = tile.x, n = tile.z;
+    if (tid < n) token[tid] = __ldcg(p.order + tile.y + tid);
+  } else {
+    pick_tile<kTcThreads, kTcTokens>(p, (int)(blockIdx.x / ranks), token, adapter, n, search);
+  }
+  fence_proxy_async_smem();                                             // tensor copies may come to `search` later
+  __syncthreads();
+  // consecutive tokens: x by tensor copies; whole 16-byte pieces too: y as well
+  const bool seq = __syncthreads_and(tid >= n || token[tid] == token[0] + tid) != 0;
+  const bool seq_y = seq && p.vec, dense = seq_y && n == kTcTokens;
+  uint64_t* full = seq ? full1 : full2;
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   const T* x = reinterpret_cast<const T*>(p.x);
@@ -203,7 +200,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int b0 = blocks * rank / ranks, b1 = blocks * (rank + 1) / ranks;
 
   if (n == 0 || adapter < 0) {                                          // the same for the whole cluster
-    if (n > 0) copy_rows(y, out, p, token, n, 128 * b0, min(128 * b1, p.N), warp, kWork + 3, lane);
+    if (n > 0) copy_rows(y, out, p, token, n, 128 * b0, min(128 * b1, p.N), warp, kWork + 3);
     __syncthreads();
     if (warp == kWork + 1) tmem_dealloc(tmem, kTcCols);
     return;
@@ -349,15 +346,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   cluster_sync();
-  // half a warp sums a row over the ranks, 8 entries a lane, and hands hi and lo to every CTA
+  // every CTA adds the partial v of all ranks for itself: half a warp a row, 8 entries a lane
   if (warp < kWork) {
     const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
-    const int l = lane & 15, rows = (kTcTokens + ranks - 1) / ranks;
-    for (int i = 2 * warp + (lane >> 4); i < (rows + 31) / 32 * 32; i += 2 * kWork) {   // whole warps, for the shuffles
-      const int r = rank * rows + i;
-      const bool mine = i < rows && r < kTcTokens;
+    const int l = lane & 15;
+    for (int r = 2 * warp + (lane >> 4); r < kTcTokens; r += 2 * kWork) {
       float v[8] = {};
-      if (mine && 8 * l < p.R) {
+      if (8 * l < p.R) {
         const uint32_t at = smem_u32(area) + (r * (p.R + 4) + 8 * l) * 4;
         float4 a[8], b[8];                                              // all ranks' loads before the first use
 #pragma unroll
@@ -386,21 +381,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       T h[8], lo[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) split(v[j] * up, h[j], lo[j]);
-      if (mine && l < 2 * steps) {
-        const uint32_t at = smem_u32(area) + C::kV + (l >> 3) * 2 * kOp + r * 128 + (((l & 7) ^ (r & 7)) << 4);
-        for (int k = 0; k < ranks; ++k) {
-          const uint32_t to = mapa_shared(at, k);
-          st_cluster_b32x4(to, *reinterpret_cast<const uint4*>(h));
-          st_cluster_b32x4(to + kOp, *reinterpret_cast<const uint4*>(lo));
-        }
+      if (l < 2 * steps) {
+        uint8_t* to = area + C::kV + (l >> 3) * 2 * kOp + r * 128 + (((l & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(h);
+        *reinterpret_cast<uint4*>(to + kOp) = *reinterpret_cast<const uint4*>(lo);
       }
-      if (mine && l == 0)
-        for (int k = 0; k < ranks; ++k) st_cluster_f32(mapa_shared(smem_u32(row_scale) + 4 * r, k), as * exp2_int(-ex));
+      if (l == 0) row_scale[r] = as * exp2_int(-ex);
     }
-    fence_proxy_async_cluster();                                        // v is read by the tensor cores
+    fence_proxy_async_smem();                                           // v is read by the tensor cores
   }
-  cluster_sync();
-  fence_proxy_async_cluster();
+  cluster_arrive();                                                     // this CTA has read the others' sums
+  __syncthreads();
 
   // ------------------------------------------------------------- expand
   if (warp < kWork) {
@@ -531,6 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
+  cluster_wait();                                                       // no CTA leaves while another reads its sums
   __syncthreads();
   if (warp == kWork + 1) {
     tc_fence_after();
