@@ -85,43 +85,33 @@ __device__ __forceinline__ void load_buckets(const int32_t* ids, int64_t i0, int
   for (int j = 0; j < E; ++j) a[j] = i0 + j >= M ? -1 : a[j] >= 0 && a[j] < L ? a[j] : L;
 }
 
-// a[j] without indexing registers by a variable.
+// The bucket that all tokens of a warp are in, or -1.
 template <int E>
-__device__ __forceinline__ int pick(const int (&a)[E], int j) {
-  int v = a[0];
+__device__ __forceinline__ int common_bucket(const int (&a)[E]) {
+  const int a0 = __shfl_sync(0xffffffffu, a[0], 0);  // (not in a condition that only some lanes evaluate)
+  bool one = a0 >= 0;
 #pragma unroll
-  for (int k = 1; k < E; ++k) v = k == j ? a[k] : v;
-  return v;
+  for (int j = 0; j < E; ++j) one = one && a[j] == a0;
+  return __all_sync(0xffffffffu, one) ? a0 : -1;
 }
 
-// Adds each token to its bucket's counter; at[j]: the counter before token j (by a whole warp). One
-// atomic where all the warp's tokens are of one bucket, else one for each run of a thread.
+// Counts a warp's tokens: one atomic where they are of one bucket, else one for each run of a thread.
 template <int E>
-__device__ __forceinline__ void take_places(int* count, const int (&a)[E], int (&at)[E]) {
-  const int lane = threadIdx.x & 31;
-  bool one = a[0] >= 0;
-#pragma unroll
-  for (int j = 1; j < E; ++j) one = one && a[j] == a[0];
-  const int a0 = __shfl_sync(0xffffffffu, a[0], 0);  // (not in a condition that only some lanes evaluate)
-  one = __all_sync(0xffffffffu, one && a[0] == a0);
-  if (one) {
-    int base = 0;
-    if (lane == 0) base = atomicAdd(&count[a[0]], 32 * E);
-    base = __shfl_sync(0xffffffffu, base, 0) + E * lane;
-#pragma unroll
-    for (int j = 0; j < E; ++j) at[j] = base + j;
+__device__ __forceinline__ void count_tokens(int* count, const int (&a)[E]) {
+  const int all = common_bucket(a);
+  if (all >= 0) {
+    if ((threadIdx.x & 31) == 0) atomicAdd(&count[all], 32 * E);
     return;
   }
-#pragma unroll 1
-  for (int j = 0; j < E;) {
-    int n = 0;                                       // a run from j on
-    const int b = pick(a, j);
-    while (j + n < E && pick(a, j + n) == b) ++n;
-    const int base = b >= 0 ? atomicAdd(&count[b], n) : 0;
+  int run = 1;
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (k >= j && k < j + n) at[k] = base + k - j;
-    j += n;
+  for (int j = 1; j <= E; ++j) {
+    if (j < E && a[j] == a[j - 1]) {
+      ++run;
+    } else {
+      if (a[j - 1] >= 0) atomicAdd(&count[a[j - 1]], run);
+      run = 1;
+    }
   }
 }
 
@@ -138,12 +128,12 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
   if (tid == 0) carry[0] = carry[1] = 0;
   grid_dep_wait();
   grid_dep_launch();
-  int a[kGroupEach], at[kGroupEach];
+  int a[kGroupEach];
   load_buckets(ids, kGroupEach * tid, M, L, a);
   __syncthreads();
   for (int r = 0; r < rounds; ++r) {
     if (r > 0) load_buckets(ids, (int64_t)kRound * r + kGroupEach * tid, M, L, a);
-    take_places(count, a, at);
+    count_tokens(count, a);
   }
   __syncthreads();
   for (int b0 = 0; b0 <= L; b0 += kGroupThreads) {   // running sums of tokens and of tiles
@@ -176,10 +166,13 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
   for (int r = 0; r < rounds; ++r) {
     const int64_t i0 = (int64_t)kRound * r + kGroupEach * tid;
     if (rounds > 1) load_buckets(ids, i0, M, L, a);
-    take_places(count, a, at);
+    const int all = common_bucket(a);
+    int base = 0;
+    if (all >= 0 && lane == 0) base = atomicAdd(&count[all], 32 * kGroupEach);
+    base = __shfl_sync(0xffffffffu, base, 0) + kGroupEach * lane;
 #pragma unroll
     for (int j = 0; j < kGroupEach; ++j)
-      if (a[j] >= 0) order[at[j]] = (int)i0 + j;
+      if (a[j] >= 0) order[all >= 0 ? base + j : atomicAdd(&count[a[j]], 1)] = (int)i0 + j;
   }
 }
 
@@ -200,11 +193,11 @@ __device__ __forceinline__ void pick_tile(const Params& p, int tile, int* token,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* sums = scratch;                               // [32]
   int* count = scratch + 32;                         // [L + 1]
-  int a[E], at[E];
+  int a[E];
   const int rounds = (p.M + kRound - 1) / kRound;
   for (int r = 0; r < rounds; ++r) {
     load_buckets(p.ids, kRound * r + E * tid, p.M, p.L, a);
-    if (__any_sync(0xffffffffu, a[0] >= 0)) take_places(count, a, at);
+    if (__any_sync(0xffffffffu, a[0] >= 0)) count_tokens(count, a);
   }
   __syncthreads();
   // every warp for itself: the bucket that holds the tile

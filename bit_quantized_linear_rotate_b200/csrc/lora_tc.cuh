@@ -84,6 +84,14 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// v is written by this CTA or by others of the cluster, and read by the tensor cores.
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_b32x4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
 // The halves of cluster_sync.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -150,6 +158,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefetch_tmap(&maps.a);
     prefetch_tmap(&maps.b);
     prefetch_tmap(&maps.x);
+    if (p.vec) {
+      prefetch_tmap(&maps.y);
+      prefetch_tmap(&maps.out);
+    }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full1[s], 1);
       mbar_init(&full2[s], 32 * kWork + 1);
@@ -285,9 +297,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tma_load_2d(area + C::kB + (s * RB + rb) * kOp, &maps.b, &bfull[s], 64 * rb, adapter * p.N + 128 * (b0 + i));
   };
   const int nb = b1 - b0;
-  if (warp == kWork && lane == 0)
-    for (int i = 0; i < min(nb, C::kStagesB); ++i) fetch_b(i);
-  __syncwarp();
   // A work warp's piece of an output block: rows 32 q .. of the tile (its TMEM lanes), columns 32 cq ..
   const int q = warp & 3, cq = warp >> 2;
   // Block i of y into its ring stage by tensor copies (one thread of warp 18) ...
@@ -321,9 +330,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   };
-  if (warp == kWork + 2 && lane == 0 && seq_y)
-    for (int i = 0; i < min(nb, C::kStagesY); ++i) copy_y(i);
-  __syncwarp();
   if (warp < kWork) {
     tc_fence_after();
     float* part = reinterpret_cast<float*>(area) + (32 * q + lane) * (p.R + 4);
@@ -340,19 +346,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     tc_fence_before();
-    if (!seq_y) {
-      if (nb > 0) fetch_y(0);                                           // while v is exchanged
+    __syncwarp();
+    cluster_arrive();
+    if (!seq_y) {                                                       // while v is exchanged
+      if (nb > 0) fetch_y(0);
       cp_async_commit();                                                // a group a block, empty ones too
     }
+  } else {                                                              // the first copies take 3 us to issue: arrive before
+    __syncwarp();
+    cluster_arrive();
+    if (warp == kWork && lane == 0)
+      for (int i = 0; i < min(nb, C::kStagesB); ++i) fetch_b(i);
+    if (warp == kWork + 2 && lane == 0 && seq_y)
+      for (int i = 0; i < min(nb, C::kStagesY); ++i) copy_y(i);
   }
-  cluster_sync();
-  // every CTA adds the partial v of all ranks for itself: half a warp a row, 8 entries a lane
+  __syncwarp();
+  cluster_wait();
+  // The partial v of all ranks, added: in a cluster of two every CTA does all rows for itself, in a larger
+  // one a share of them for all (reading everything from everybody took 9 us in a cluster of 8, this 3).
+  // A power of two of lanes a row, 8 entries a lane.
   if (warp < kWork) {
     const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
-    const int l = lane & 15;
-    for (int r = 2 * warp + (lane >> 4); r < kTcTokens; r += 2 * kWork) {
+    int lw = 1;
+    while (1 << lw < 2 * steps) ++lw;
+    const int l = lane & ((1 << lw) - 1), per = 32 >> lw;
+    const bool alone = ranks <= 2;
+    const int rows = alone ? kTcTokens : (kTcTokens + ranks - 1) / ranks, r0 = alone ? 0 : rank * rows;
+    const int d0 = alone ? rank : 0, d1 = alone ? rank + 1 : ranks;     // the CTAs that get the sums
+    for (int i = per * warp + (lane >> lw); i < (rows + per - 1) / per * per; i += per * kWork) {   // whole warps
+      const int r = r0 + i;
+      const bool mine = i < rows && r < kTcTokens;
       float v[8] = {};
-      if (8 * l < p.R) {
+      if (mine && 8 * l < p.R) {
         const uint32_t at = smem_u32(area) + (r * (p.R + 4) + 8 * l) * 4;
         float4 a[8], b[8];                                              // all ranks' loads before the first use
 #pragma unroll
@@ -374,24 +399,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = 1; o < 16; o <<= 1)
+          if (o >> lw == 0) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         ex = scale_exponent(top);
       }
       const float up = exp2_int(ex);
       T h[8], lo[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) split(v[j] * up, h[j], lo[j]);
-      if (l < 2 * steps) {
-        uint8_t* to = area + C::kV + (l >> 3) * 2 * kOp + r * 128 + (((l & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(h);
-        *reinterpret_cast<uint4*>(to + kOp) = *reinterpret_cast<const uint4*>(lo);
+      if (mine && l < 2 * steps) {
+        const uint32_t at = smem_u32(area) + C::kV + (l >> 3) * 2 * kOp + r * 128 + (((l & 7) ^ (r & 7)) << 4);
+        for (int k = d0; k < d1; ++k) {
+          const uint32_t to = mapa_shared(at, k);
+          st_cluster_b32x4(to, *reinterpret_cast<const uint4*>(h));
+          st_cluster_b32x4(to + kOp, *reinterpret_cast<const uint4*>(lo));
+        }
       }
-      if (l == 0) row_scale[r] = as * exp2_int(-ex);
+      if (mine && l == 0)
+        for (int k = d0; k < d1; ++k) st_cluster_f32(mapa_shared(smem_u32(row_scale) + 4 * r, k), as * exp2_int(-ex));
     }
-    fence_proxy_async_smem();                                           // v is read by the tensor cores
+    fence_proxy_async_cluster();                                        // v is read by the tensor cores
   }
-  cluster_arrive();                                                     // this CTA has read the others' sums
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();
+  fence_proxy_async_cluster();
 
   // ------------------------------------------------------------- expand
   if (warp < kWork) {
@@ -522,7 +553,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  cluster_wait();                                                       // no CTA leaves while another reads its sums
   __syncthreads();
   if (warp == kWork + 1) {
     tc_fence_after();
