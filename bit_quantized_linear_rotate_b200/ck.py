@@ -176,9 +176,6 @@ def last_error() -> str:
 
 def _call(dev, name: str, *args, stream=None) -> None:
     """Calls the C entry point `name` with `dev` current and that device's stream appended."""
-    if stream is None and torch.cuda.current_device() == dev.index:     # the common case, without a device guard
-        _check(getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
-        return
     with torch.cuda.device(dev):
         _check(getattr(lib, name)(*args, _stream(stream, dev)), name)
 
@@ -449,16 +446,21 @@ def gemv_awq_w4a16(x, qweight, wscales, wzeros, bias=None, group_size: int = 64,
 
 
 # ------------------------------------------ weights chosen for each token
+#
+# These calls are short (some 5 us on the device), so their checks are one expression over cheap
+# attributes; only when it fails does a slower function find out what is wrong and say so.
 
 _LOGITS = (torch.bfloat16, torch.float16, torch.float32)
+_f32t, _i32t, _bf16t = torch.float32, torch.int32, torch.bfloat16
+_byte_like = frozenset(_BYTES)
 
 
-def _empty(shape, dtype, dev, stream):
+def _empty(like, shape, dtype, stream):
     """A tensor for the call's own use or its result, from the pool of the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _shape(where: str, **named) -> None:
@@ -469,16 +471,41 @@ def _shape(where: str, **named) -> None:
                              f"{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
-def _matrix(where: str, name: str, t, cols=None) -> None:
-    """ValueError unless t is 2-D with a contiguous last dimension (of `cols` entries)."""
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{where}: {name} must be a 2-D tensor with contiguous rows"
-                         f"{'' if cols is None else f' of {cols} entries'}, got {tuple(t.shape)}")
+def _matrix(where: str, name: str, t, rows, cols) -> None:
+    """ValueError unless t is (rows, cols) with a contiguous last dimension."""
+    if tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{where}: {name} must be ({rows}, {cols}) with contiguous rows, got {tuple(t.shape)} with "
+                         f"strides {t.stride()}")
 
 
-def _ld(t) -> int:
-    """Row stride of a 2-D tensor; that of a single row is its length whatever the tensor says."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _on(dev: int, *ts) -> bool:
+    """Whether all given tensors (None is skipped) live on CUDA device `dev`."""
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            return False
+    return dev >= 0
+
+
+def _run(fn, name: str, dev: int, stream, *args) -> None:
+    """_call for a C function at hand and a device index."""
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        device = torch.device("cuda", dev)
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(stream, device))
+    if status != CK_OK:
+        raise CKError(status, name)
+
+
+def _no_route(logits, top_k, weights_out, ids_out):
+    """Raises what is wrong with moe_route's arguments."""
+    _types("moe_route", logits=(logits, _LOGITS), weights_out=(weights_out, _F32), ids_out=(ids_out, _I32))
+    if logits.dim() != 2:
+        raise ValueError(f"moe_route: logits must be (T, E), got {tuple(logits.shape)}")
+    T, E = logits.shape
+    _shape("moe_route", logits=(logits, (T, E)), weights_out=(weights_out, (T, top_k)), ids_out=(ids_out, (T, top_k)))
+    _cuda(logits, weights_out, ids_out)
 
 
 def moe_route(logits, top_k: int, renormalize: bool = True, weights_out=None, ids_out=None, stream=None):
@@ -486,17 +513,17 @@ def moe_route(logits, top_k: int, renormalize: bool = True, weights_out=None, id
 
     weights are softmax shares among the chosen (renormalize) or among all E experts; ties go to the
     lowest index; a -inf or NaN logit is never chosen, and a slot left over has id -1 and weight 0."""
-    _types("moe_route", logits=(logits, _LOGITS), weights_out=(weights_out, _F32), ids_out=(ids_out, _I32))
-    if logits.dim() != 2:
-        raise ValueError(f"moe_route: logits must be (T, E), got {tuple(logits.shape)}")
+    top_k = int(top_k)
+    dev = logits.get_device()
+    if not (logits.dtype in _LOGITS and logits.dim() == 2 and logits.is_contiguous() and dev >= 0
+            and weights_out is None and ids_out is None):
+        _no_route(logits, top_k, weights_out, ids_out)
     T, E = logits.shape
-    _shape("moe_route", logits=(logits, (T, E)), weights_out=(weights_out, (T, top_k)), ids_out=(ids_out, (T, top_k)))
-    dev = _cuda(logits, weights_out, ids_out)
-    k = max(int(top_k), 0)
-    weights = _empty((T, k), torch.float32, dev, stream) if weights_out is None else weights_out
-    ids = _empty((T, k), torch.int32, dev, stream) if ids_out is None else ids_out
-    _call(dev, "ck_moe_route", logits.data_ptr(), _LOGITS.index(logits.dtype), T, E, int(top_k), int(bool(renormalize)),
-          weights.data_ptr(), ids.data_ptr(), stream=stream)
+    k = max(top_k, 0)
+    weights = _empty(logits, (T, k), _f32t, stream) if weights_out is None else weights_out
+    ids = _empty(logits, (T, k), _i32t, stream) if ids_out is None else ids_out
+    _run(lib.ck_moe_route, "ck_moe_route", dev, stream, logits.data_ptr(), _LOGITS.index(logits.dtype), T, E, top_k,
+         1 if renormalize else 0, weights.data_ptr(), ids.data_ptr())
     return weights, ids
 
 
@@ -504,32 +531,58 @@ def moe_awq_w4a16_workspace_bytes(T: int, top_k: int, K: int, I: int) -> int:
     return int(lib.ck_moe_awq_w4a16_workspace_bytes(T, top_k, K, I))
 
 
-def _moe(name, x, given, choice, top_k, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, group_size, workspace, out,
-         stream):
-    """Shared marshalling of the mixture-of-experts calls; `given` are the tensors of the choice, `choice`
-    the C arguments between the group size and the weights."""
+def _no_moe(name, x, given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, G, workspace, out):
+    """Raises what is wrong with a mixture-of-experts call's arguments (its choice apart)."""
     same = (x.dtype,) if x.dtype in _HALF else _HALF
     _types(name, x=(x, _HALF), gate_up_q=(gate_up_q, _BYTES), gate_up_s=(gate_up_s, same), gate_up_z=(gate_up_z, same),
            down_q=(down_q, _BYTES), down_s=(down_s, same), down_z=(down_z, same), out=(out, same),
            workspace=(workspace, _BYTES))
-    _matrix(name, "x", x)
+    if x.dim() != 2 or gate_up_q.dim() != 3 or gate_up_q.shape[1] % 2:
+        raise ValueError(f"{name}: x must be (T, K) and gate_up_q (E, 2 I, K / 2), got {tuple(x.shape)} and "
+                         f"{tuple(gate_up_q.shape)}")
     T, K = x.shape
-    if gate_up_q.dim() != 3 or gate_up_q.shape[1] % 2:
-        raise ValueError(f"{name}: gate_up_q must be (E, 2 I, K / 2), got {tuple(gate_up_q.shape)}")
     E, I = gate_up_q.shape[0], gate_up_q.shape[1] // 2
-    G = int(group_size)
+    _matrix(name, "x", x, T, K)
     if G > 0:
         _shape(name, gate_up_q=(gate_up_q, (E, 2 * I, K // 2)), gate_up_s=(gate_up_s, (E, K // G, 2 * I)),
                gate_up_z=(gate_up_z, (E, K // G, 2 * I)), down_q=(down_q, (E, K, I // 2)),
                down_s=(down_s, (E, I // G, K)), down_z=(down_z, (E, I // G, K)), out=(out, (T, K)))
-    dev = _cuda(x, *given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, workspace, out)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"{name}: workspace must be contiguous")
+    _cuda(x, *given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, workspace, out)
+
+
+def _moe(fn, name, x, given, choice, top_k, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, group_size,
+         workspace, out, stream):
+    """Shared marshalling of the mixture-of-experts calls; `given` are the tensors of the choice, `choice`
+    the C arguments between the group size and the weights."""
+    G = int(group_size)
+    dt = x.dtype
+    dev = x.get_device()
+    fast = (x.dim() == 2 and gate_up_q.dim() == 3 and G > 0 and dt in _HALF and gate_up_s.dtype == dt
+            and gate_up_z.dtype == dt and down_s.dtype == dt and down_z.dtype == dt and gate_up_q.dtype in _byte_like
+            and down_q.dtype in _byte_like and workspace is None and out is None)
+    if fast:
+        T, K = x.shape
+        E, I = gate_up_q.shape[0], gate_up_q.shape[1] >> 1
+        Kh, Kg, Ig = K >> 1, K // G, I // G
+        fast = (gate_up_q.shape == (E, 2 * I, Kh) and gate_up_s.shape == (E, Kg, 2 * I)
+                and gate_up_z.shape == gate_up_s.shape and down_q.shape == (E, K, I >> 1)
+                and down_s.shape == (E, Ig, K) and down_z.shape == down_s.shape and gate_up_q.is_contiguous() and gate_up_s.is_contiguous()
+                and gate_up_z.is_contiguous() and down_q.is_contiguous() and down_s.is_contiguous()
+                and down_z.is_contiguous() and (x.stride(1) == 1 or K <= 1)
+                and _on(dev, *given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z))
+    if not fast:
+        _no_moe(name, x, given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, G, workspace, out)
+        T, K = x.shape
+        E, I = gate_up_q.shape[0], gate_up_q.shape[1] >> 1
     if workspace is None:
-        workspace = _empty((moe_awq_w4a16_workspace_bytes(T, top_k, K, I),), torch.uint8, dev, stream)
+        workspace = _empty(x, (int(lib.ck_moe_awq_w4a16_workspace_bytes(T, top_k, K, I)),), torch.uint8, stream)
     if out is None:
-        out = _empty((T, K), x.dtype, dev, stream)
-    _call(dev, "ck_" + name, x.data_ptr(), _dtype_code(x.dtype), T, K, I, E, _ld(x), G, *choice, gate_up_q.data_ptr(),
-          gate_up_s.data_ptr(), gate_up_z.data_ptr(), down_q.data_ptr(), down_s.data_ptr(), down_z.data_ptr(),
-          out.data_ptr(), workspace.data_ptr(), _nbytes(workspace), stream=stream)
+        out = _empty(x, (T, K), dt, stream)
+    _run(fn, name, dev, stream, x.data_ptr(), 0 if dt == _bf16t else 1, T, K, I, E, x.stride(0) if T > 1 else K, G,
+         *choice, gate_up_q.data_ptr(), gate_up_s.data_ptr(), gate_up_z.data_ptr(), down_q.data_ptr(),
+         down_s.data_ptr(), down_z.data_ptr(), out.data_ptr(), workspace.data_ptr(), _nbytes(workspace))
     return out
 
 
@@ -541,11 +594,14 @@ def moe_awq_w4a16(x, logits, top_k: int, gate_up_q, gate_up_s, gate_up_z, down_q
     The experts are AWQ W4A16: gate_up_q (E, 2 I, K/2) packed bytes, the gate rows first, with scales and
     zeros (E, K/G, 2 I); down_q (E, K, I/2) with scales and zeros (E, I/G, K), all in x's dtype."""
     name = "moe_awq_w4a16"
-    _types(name, logits=(logits, _LOGITS))
-    _shape(name, logits=(logits, (x.shape[0], gate_up_q.shape[0])))
-    choice = (logits.data_ptr(), _LOGITS.index(logits.dtype), int(top_k), int(bool(renormalize)))
-    return _moe(name, x, (logits,), choice, int(top_k), gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z,
-                group_size, workspace, out, stream)
+    top_k = int(top_k)
+    if not (logits.dtype in _LOGITS and logits.is_contiguous() and logits.dim() == 2
+            and logits.shape[0] == x.shape[0] and logits.shape[1] == gate_up_q.shape[0]):
+        _types(name, logits=(logits, _LOGITS))
+        _shape(name, logits=(logits, (x.shape[0], gate_up_q.shape[0])))
+    choice = (logits.data_ptr(), _LOGITS.index(logits.dtype), top_k, 1 if renormalize else 0)
+    return _moe(lib.ck_moe_awq_w4a16, name, x, (logits,), choice, top_k, gate_up_q, gate_up_s, gate_up_z, down_q,
+                down_s, down_z, group_size, workspace, out, stream)
 
 
 def moe_experts_awq_w4a16(x, ids, weights, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z,
@@ -553,17 +609,38 @@ def moe_experts_awq_w4a16(x, ids, weights, gate_up_q, gate_up_s, gate_up_z, down
     """moe_awq_w4a16 with the choice given: ids (T, top_k) int32 and weights (T, top_k) float32, used as they
     are. A slot whose id is outside [0, E) is empty; an expert named twice counts with both weights."""
     name = "moe_experts_awq_w4a16"
-    _types(name, ids=(ids, _I32), weights=(weights, _F32))
-    if ids.dim() != 2:
-        raise ValueError(f"{name}: ids must be (T, top_k), got {tuple(ids.shape)}")
+    if not (ids.dtype == _i32t and weights.dtype == _f32t and ids.dim() == 2 and ids.shape[0] == x.shape[0]
+            and weights.shape == ids.shape and ids.is_contiguous() and weights.is_contiguous()):
+        _types(name, ids=(ids, _I32), weights=(weights, _F32))
+        if ids.dim() != 2:
+            raise ValueError(f"{name}: ids must be (T, top_k), got {tuple(ids.shape)}")
+        _shape(name, ids=(ids, (x.shape[0], ids.shape[1])), weights=(weights, (x.shape[0], ids.shape[1])))
     k = ids.shape[1]
-    _shape(name, ids=(ids, (x.shape[0], k)), weights=(weights, (x.shape[0], k)))
-    return _moe(name, x, (ids, weights), (ids.data_ptr(), weights.data_ptr(), k), k, gate_up_q, gate_up_s, gate_up_z,
-                down_q, down_s, down_z, group_size, workspace, out, stream)
+    return _moe(lib.ck_moe_experts_awq_w4a16, name, x, (ids, weights), (ids.data_ptr(), weights.data_ptr(), k), k,
+                gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, group_size, workspace, out, stream)
 
 
 def lora_add_workspace_bytes(M: int, L: int) -> int:
     return int(lib.ck_lora_add_workspace_bytes(M, L))
+
+
+def _no_lora(y, x, lora_a, lora_b, ids, scales, workspace, out):
+    """Raises what is wrong with lora_add's arguments."""
+    same = (x.dtype,) if x.dtype in _HALF else _HALF
+    _types("lora_add", y=(y, same + _BF16), x=(x, _HALF), lora_a=(lora_a, same), lora_b=(lora_b, same), ids=(ids, _I32),
+           scales=(scales, _F32), out=(out, (y.dtype,)), workspace=(workspace, _BYTES))
+    if x.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
+        raise ValueError("lora_add: x must be (M, K), lora_a (L, R, K) and lora_b (L, N, R)")
+    (M, K), (L, R) = x.shape, lora_a.shape[:2]
+    N = lora_b.shape[1]
+    _matrix("lora_add", "x", x, M, K)
+    _matrix("lora_add", "y", y, M, N)
+    if out is not None:
+        _matrix("lora_add", "out", out, M, N)
+    _shape("lora_add", lora_a=(lora_a, (L, R, K)), lora_b=(lora_b, (L, N, R)), ids=(ids, (M,)), scales=(scales, (L,)))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("lora_add: workspace must be contiguous")
+    _cuda(y, x, lora_a, lora_b, ids, scales, workspace, out)
 
 
 def lora_add(y, x, lora_a, lora_b, ids, scales=None, workspace=None, out=None, stream=None):
@@ -571,37 +648,32 @@ def lora_add(y, x, lora_a, lora_b, ids, scales=None, workspace=None, out=None, s
 
     y (M, N) bf16 or x's dtype is a projection's output, x (M, K) its input; lora_a (L, R, K) and lora_b
     (L, N, R) are the adapters, ids (M,) int32 (-1: none), scales (L,) float32. `out` may be y: in place."""
-    same = (x.dtype,) if x.dtype in _HALF else _HALF
-    half = same + _BF16
-    _types("lora_add", y=(y, half), x=(x, _HALF), lora_a=(lora_a, same), lora_b=(lora_b, same), ids=(ids, _I32),
-           scales=(scales, _F32), out=(out, (y.dtype,)), workspace=(workspace, _BYTES))
-    _matrix("lora_add", "x", x)
+    dt, ydt = x.dtype, y.dtype
+    dev = x.get_device()
+    if not (x.dim() == 2 and lora_a.dim() == 3 and lora_b.dim() == 3 and dt in _HALF and lora_a.dtype == dt
+            and lora_b.dtype == dt and (ydt == dt or ydt == _bf16t) and ids.dtype == _i32t
+            and ids.shape == x.shape[:1] and ids.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous()
+            and lora_a.shape[2] == x.shape[1] and lora_b.shape[0] == lora_a.shape[0]
+            and lora_b.shape[2] == lora_a.shape[1] and y.shape == (x.shape[0], lora_b.shape[1])
+            and x.is_contiguous() and y.is_contiguous() and workspace is None and (out is None or out is y)
+            and (scales is None or (scales.dtype == _f32t and scales.shape == lora_a.shape[:1]
+                                    and scales.is_contiguous()))
+            and _on(dev, y, lora_a, lora_b, ids, scales)):
+        _no_lora(y, x, lora_a, lora_b, ids, scales, workspace, out)
     M, K = x.shape
-    if lora_a.dim() != 3 or lora_b.dim() != 3:
-        raise ValueError("lora_add: lora_a must be (L, R, K) and lora_b (L, N, R)")
-    L, R = lora_a.shape[:2]
-    N = lora_b.shape[1]
-    _matrix("lora_add", "y", y, N)
-    if y.shape[0] != M:
-        raise ValueError(f"lora_add: y has {y.shape[0]} rows, x {M}")
-    _shape("lora_add", lora_a=(lora_a, (L, R, K)), lora_b=(lora_b, (L, N, R)), ids=(ids, (M,)), scales=(scales, (L,)))
-    dev = _cuda(y, x, lora_a, lora_b, ids, scales, workspace, out)
+    L, N, R = lora_b.shape
     if out is None:
-        out = _empty((M, N), y.dtype, dev, stream)
-    else:
-        _matrix("lora_add", "out", out, N)
-        if out.shape[0] != M:
-            raise ValueError(f"lora_add: out has {out.shape[0]} rows, x {M}")
+        out = _empty(y, (M, N), ydt, stream)
     if workspace is None:
-        need = lora_add_workspace_bytes(M, L)
-        ws_ptr, ws_bytes = None, 0
+        need = lib.ck_lora_add_workspace_bytes(M, L)
         if need:
-            workspace = _empty((need,), torch.uint8, dev, stream)
-    if workspace is not None:
-        ws_ptr, ws_bytes = workspace.data_ptr(), _nbytes(workspace)
-    _call(dev, "ck_lora_add", y.data_ptr(), _dtype_code(y.dtype), x.data_ptr(), _dtype_code(x.dtype), M, K, N, R, L,
-          _ld(x), _ld(y), _ld(out), lora_a.data_ptr(), lora_b.data_ptr(), ids.data_ptr(),
-          None if scales is None else scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes, stream=stream)
+            workspace = _empty(x, (need,), torch.uint8, stream)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), _nbytes(workspace))
+    one = M <= 1                                  # the stride of a single row is its length, whatever the tensor says
+    _run(lib.ck_lora_add, "ck_lora_add", dev, stream, y.data_ptr(), 0 if ydt == _bf16t else 1, x.data_ptr(),
+         0 if dt == _bf16t else 1, M, K, N, R, L, K if one else x.stride(0), N if one else y.stride(0),
+         N if one else out.stride(0), lora_a.data_ptr(), lora_b.data_ptr(), ids.data_ptr(),
+         None if scales is None else scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes)
     return out
 
 

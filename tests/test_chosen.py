@@ -258,8 +258,14 @@ def test_binding_refuses_shapes_and_dtypes_before_any_launch(ck):
         ck.lora_add(y, x, a, b, ids.long())
     with pytest.raises(ValueError, match="lora_b"):
         ck.lora_add(y, x, a, b[:, :, :4].contiguous(), ids)
-    with pytest.raises(ValueError, match="rows"):
+    with pytest.raises(ValueError, match="y must be"):
         ck.lora_add(y[:3], x, a, b, ids)
+    with pytest.raises(ValueError, match="y must be"):
+        ck.lora_add(y.t().contiguous().t(), x, a, b, ids)    # columns are contiguous, rows are not
+    with pytest.raises(ValueError, match="x must be"):
+        ck.lora_add(y, x[0], a, b, ids)
+    with pytest.raises(ValueError, match="scales"):
+        ck.lora_add(y, x, a, b, ids, scales=torch.zeros(2))
     with pytest.raises(ValueError, match="ids"):
         ck.lora_add(y, x, a, b, ids[:3])
     with pytest.raises(TypeError, match="out"):
