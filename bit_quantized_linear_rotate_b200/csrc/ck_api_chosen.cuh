@@ -65,7 +65,9 @@ template <typename T, int NT, int KW, bool SELF>
 cudaError_t launch_gate_up(const ck::moe::Maps& maps, const ck::moe::Params& p, cudaStream_t st) {
   using namespace ck::moe;
   using C = GateUp<NT, KW, SELF>;
-  auto kern = gate_up_kernel<T, NT, KW, SELF>;
+  void (*kern)(const Maps, const Params, int);
+  if constexpr (SELF) kern = gate_up_few_kernel<T>;
+  else kern = gate_up_kernel<T, NT>;
   struct Tag {};
   const int offset = ring_offset(p.choice.T * p.choice.k, C::sums(p.choice.T, p.K));
   int ctas = C::kCtas;
@@ -125,7 +127,8 @@ struct MoeWorkspace {
 // tokens an expert is likely to get, the mean and three standard deviations: an expert with
 // more is read again for the rest, while room for 16 tokens in every stage costs depth of the ring.
 bool moe_self(const ck::moe::Params& p) {
-  return p.choice.T <= ck::moe::kFewTokens && p.choice.T * ck::moe::row_bytes(p.K) <= ck::moe::kSelfBytes;
+  return p.choice.T <= ck::moe::kFewTokens && p.choice.T * p.choice.k <= ck::moe::kFewSlots &&
+         p.choice.T * ck::moe::row_bytes(p.K) <= ck::moe::kSelfBytes;
 }
 int moe_token_tiles(const ck::moe::Params& p) {
   const double mean = (double)p.choice.T * p.choice.k / p.choice.E;

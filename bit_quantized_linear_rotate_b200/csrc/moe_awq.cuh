@@ -290,13 +290,12 @@ struct GateUp {
   static constexpr int kRows = SELF ? 0 : 4 * NT * (kSubs / 4) * kRecord;
   static constexpr int kStage = (2 * kW + 4 * kS + kRows + 1023) / 1024 * 1024;
   static constexpr int kRed = KW * 4 * 2 * NT * 32 * 8;         // float2 [kw][rq][gate, up][token tile][lane]
-  static_assert(sizeof(FewTemp) <= kRed, "build_few works in it");
+  static_assert(sizeof(FewTemp) <= kRed, "the choice is handed on in it");
   __host__ __device__ static constexpr int sums(int T, int K) { return kRed + (SELF ? T * row_bytes(K) : 0); }
 };
 
 template <typename T, int NT, int KW, bool SELF>
-__global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW, SELF>::kCtas)
-    gate_up_kernel(const __grid_constant__ Maps maps, const Params p, int stages) {
+__device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int stages) {
   using C = GateUp<NT, KW, SELF>;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = align_1024(sm_raw);
@@ -316,13 +315,26 @@ __global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW,
   }
   grid_dep_wait();
   grid_dep_launch();   // after the wait: the next kernel may read the choice before its own wait
-  if constexpr (SELF) build_few(p.choice, L, *reinterpret_cast<FewTemp*>(red));
-  else copy_lists<C::kThreads>(sm + kHead, p.lists, slots);
+  const int xrow = row_bytes(p.K);
+  if constexpr (SELF) {                // warps 0-3 choose while the others convert x
+    FewTemp& few = *reinterpret_cast<FewTemp*>(red);
+    constexpr int kConvert = C::kThreads - 32 * kFewTokens;
+    if (warp < kFewTokens) {
+      choose_few(p.choice, few);
+    } else {
+      for (int i = 0; i < tokens; ++i)
+        convert_row<T, kConvert>(reinterpret_cast<const T*>(p.x) + i * p.ldx, p.K, own + i * xrow, tid - 32 * kFewTokens);
+    }
+    __syncthreads();
+    list_few(p.choice, L, few);
+    __syncthreads();
+  } else {
+    copy_lists<C::kThreads>(sm + kHead, p.lists, slots);
+  }
 
   const int per_unit = p.I / kColsItem, nsub = p.K >> 6, nchunk = (nsub + C::kSubs - 1) / C::kSubs;
   const int items = L.units() * per_unit;
   const int srows = C::kSubs >> p.gsh;   // rows of scales a stage: its columns' groups
-  const int xrow = row_bytes(p.K);
 
   if (warp == C::kCons) {
     fence_proxy_async_all();
@@ -363,12 +375,6 @@ __global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW,
     }
     if (!live && lane == 0) ring_drain(R, at, stages, issued);
     return;
-  }
-
-  if constexpr (SELF) {
-    for (int i = 0; i < tokens; ++i)
-      convert_row<T, 32 * C::kCons>(reinterpret_cast<const T*>(p.x) + i * p.ldx, p.K, own + i * xrow, tid);
-    consumers_sync<32 * C::kCons>();
   }
 
   const int kw = warp >> 2, rq = warp & 3;
@@ -465,6 +471,20 @@ __global__ void __launch_bounds__(GateUp<NT, KW, SELF>::kThreads, GateUp<NT, KW,
   }
 }
 
+template <typename T, int NT>
+__global__ void __launch_bounds__(GateUp<NT, 2, false>::kThreads, GateUp<NT, 2, false>::kCtas)
+    gate_up_kernel(const __grid_constant__ Maps maps, const Params p, int stages) {
+  gate_up<T, NT, 2, false>(maps, p, stages);
+}
+
+// 64 registers: a CTA of down_kernel fits beside this one's, and builds its lists and fetches its first weights
+// while this kernel runs.
+template <typename T>
+__global__ void __maxnreg__(64)
+    gate_up_few_kernel(const __grid_constant__ Maps maps, const Params p, int stages) {
+  gate_up<T, 1, 4, true>(maps, p, stages);
+}
+
 // --------------------------------------------------------------------- down
 
 // A cluster of CTAs owns 64 output columns and walks (unit, 256 SUB columns of h)
@@ -504,10 +524,18 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
     prefetch_tmap(&maps.z);
     ring_init(R, stages, C::kCons);
   }
-  for (int i = tid; i < 4 * cells; i += C::kThreads) sums[i] = 0.0f;
   // The choice and the lists were complete before gate_up_kernel let this kernel start.
-  if (p.lists == nullptr) build_few(p.choice, L, *reinterpret_cast<FewTemp*>(ring));
-  else copy_lists<C::kThreads>(sm + kHead, p.lists, slots);
+  if (p.lists == nullptr) {
+    FewTemp& few = *reinterpret_cast<FewTemp*>(sums);   // (cleared below)
+    choose_few(p.choice, few);
+    __syncthreads();
+    list_few(p.choice, L, few);
+    __syncthreads();
+  } else {
+    copy_lists<C::kThreads>(sm + kHead, p.lists, slots);
+  }
+  for (int i = tid; i < 4 * cells; i += C::kThreads) sums[i] = 0.0f;
+  __syncthreads();
 
   const int nsub = p.I >> 6, nchunk = (nsub + C::kSubs - 1) / C::kSubs;
   const int srows = C::kSubs >> p.gsh;
@@ -649,8 +677,11 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
   cluster_sync();
   const uint32_t base = smem_u32(sums);
   for (int i = rank * C::kThreads + tid; i < cells; i += ranks * C::kThreads) {
-    float v = 0.0f;
-    for (uint32_t r = 0; r < ranks; ++r) v += ld_cluster_f32(mapa_shared(base + 4 * i, r));
+    float part[8], v = 0.0f;                        // all loads before the first sum
+#pragma unroll
+    for (uint32_t r = 0; r < 8; ++r) part[r] = r < ranks ? ld_cluster_f32(mapa_shared(base + 4 * i, r)) : 0.0f;
+#pragma unroll
+    for (uint32_t r = 0; r < 8; ++r) v += part[r];
     reinterpret_cast<T*>(p.out)[(int64_t)(i / kRowsTile) * p.K + n0 + i % kRowsTile] = awq::Traits<T>::fromf(v);
   }
   cluster_sync();                                   // no CTA leaves while another reads its sums

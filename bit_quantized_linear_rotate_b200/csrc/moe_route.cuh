@@ -238,81 +238,79 @@ __device__ __forceinline__ void build_lists(const Choice& c, const Lists& L, Lis
   __syncthreads();
 }
 
-// The same for at most 64 slots of at most four tokens, by T warps and then one, where
-// an expert is one unit (cap >= 4): units are in the order in which the slots
-// first name them. Every CTA of both kernels of a small batch builds them (3.3 us
-// by build_lists); closes with a barrier.
-constexpr int kFewTokens = 4;
+// The same for at most 32 slots of at most four tokens, by warp 0, a slot a lane, from the choice in
+// tmp (choose_few and a barrier before it). An expert is one unit (cap >= 4), in the order in
+// which the slots first name them. Every CTA of both kernels of a small batch builds them
+// (3.3 us by build_lists, most of it barriers and waits on shared memory; 0.3 so).
+constexpr int kFewTokens = 4, kFewSlots = 32;
 struct FewTemp {
-  float w[kFewTokens * kMaxTopK];
-  int id[kFewTokens * kMaxTopK], n[kFewTokens * kMaxTopK];
+  float w[kFewSlots];
+  int id[kFewSlots];
 };
-__device__ __forceinline__ void build_few(const Choice& c, const Lists& L, FewTemp& tmp) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slots = c.T * c.k;
-  if (warp < c.T) {
-    int id = -1;
-    float w = 0.0f;
-    if (c.ids == nullptr) {
-      choose_any(c.logits, c.ldt, warp, c.E, c.k, c.renorm != 0, id, w);
-    } else if (lane < c.k) {
-      id = __ldcg(c.ids + warp * c.k + lane);
-      if (id < 0 || id >= c.E) id = -1;
-      w = __ldcg(c.weights + warp * c.k + lane);
-    }
-    if (lane < c.k) {
-      tmp.id[warp * c.k + lane] = id;
-      tmp.w[warp * c.k + lane] = w;
-    }
+
+// Warp t < T: token t's choice into tmp.
+__device__ __forceinline__ void choose_few(const Choice& c, FewTemp& tmp) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp >= c.T) return;
+  int id = -1;
+  float w = 0.0f;
+  if (c.ids == nullptr) {
+    choose_any(c.logits, c.ldt, warp, c.E, c.k, c.renorm != 0, id, w);
+  } else if (lane < c.k) {
+    id = __ldcg(c.ids + warp * c.k + lane);
+    if (id < 0 || id >= c.E) id = -1;
+    w = __ldcg(c.weights + warp * c.k + lane);
   }
-  __syncthreads();
-  if (warp == 0) {
-    unsigned tokens[2];
-    int units = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int s = lane + 32 * h, e = s < slots ? tmp.id[s] : -1;
-      bool first = e >= 0;                           // whether the slot is its expert's first
-      tokens[h] = 0;
-      if (e >= 0)
-        for (int j = 0, t = 0, in = 0; j < slots; ++j) {
-          if (tmp.id[j] == e) {
-            tokens[h] |= 1u << t;
-            if (j < s) first = false;
-          }
-          if (++in == c.k) in = 0, ++t;
-        }
-      if (s < slots) tmp.n[s] = first ? __popc(tokens[h]) : 0;
-      if (!first) tokens[h] = 0;
-      units += __popc(__ballot_sync(0xffffffffu, first));
-    }
-    __syncwarp();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (tokens[h] == 0) continue;
-      const int s = lane + 32 * h, e = tmp.id[s];
-      int unit = 0, slot = 0;
-      for (int j = 0; j < s; ++j) {
-        const int n = tmp.n[j];
-        unit += n != 0;
-        slot += n;
-      }
-      L.unit_expert[unit] = (uint16_t)e;
-      L.unit_start[unit] = (uint16_t)slot;
-      L.unit_n[unit] = (uint8_t)__popc(tokens[h]);
-      for (unsigned m = tokens[h]; m != 0; m &= m - 1, ++slot) {
-        const int t = __ffs(m) - 1;
-        float w = 0.0f;
-        for (int j = 0; j < c.k; ++j)
-          if (tmp.id[t * c.k + j] == e) w += tmp.w[t * c.k + j];
-        L.slot_token[slot] = (uint8_t)t;
-        L.slot_w[slot] = w;
-      }
-    }
-    if (lane == 0) L.scratch[32] = units;
+  if (lane < c.k) {
+    tmp.id[warp * c.k + lane] = id;
+    tmp.w[warp * c.k + lane] = w;
   }
-  fence_proxy_async_smem();                          // tmp may become the target of tensor copies
-  __syncthreads();
+}
+
+__device__ __forceinline__ void list_few(const Choice& c, const Lists& L, const FewTemp& tmp) {
+  if (threadIdx.x >= 32) return;
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x;
+  const unsigned below = (1u << lane) - 1;
+  const bool in = lane < c.T * c.k;
+  const int e = in ? tmp.id[lane] : -1, t = in ? lane / c.k : 0;
+  const float w = in ? tmp.w[lane] : 0.0f;
+  const bool live = e >= 0;
+  const unsigned same = __match_any_sync(kAll, live ? e : -1 - lane);            // slots of this expert
+  const unsigned twin = __match_any_sync(kAll, live ? 4 * e + t : -1 - lane);    // of this expert and token
+  float sum = 0.0f;                                  // the twins' weights, in order
+  for (unsigned left = __reduce_or_sync(kAll, __popc(twin) > 1 ? twin : 0u); left != 0; left &= left - 1) {
+    const int j = __ffs(left) - 1;
+    const float v = __shfl_sync(kAll, w, j);
+    if (twin >> j & 1) sum += v;
+  }
+  if (__popc(twin) == 1) sum = w;
+  const bool first = live && (same & below) == 0, first_twin = live && (twin & below) == 0;
+  unsigned tokens = 0;                               // of this expert
+#pragma unroll
+  for (int i = 0; i < kFewTokens; ++i)
+    if (__ballot_sync(kAll, live && t == i) & same) tokens |= 1u << i;
+  const int n = __popc(tokens);
+  int start = first ? n : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(kAll, start, o);
+    if (lane >= o) start += u;
+  }
+  start = __shfl_sync(kAll, start - n, __ffs(same) - 1);      // the leader's: slots before this expert's
+  const unsigned leaders = __ballot_sync(kAll, first);
+  if (first) {
+    const int unit = __popc(leaders & below);
+    L.unit_expert[unit] = (uint16_t)e;
+    L.unit_start[unit] = (uint16_t)start;
+    L.unit_n[unit] = (uint8_t)n;
+  }
+  if (first_twin) {
+    const int slot = start + __popc(tokens & ((1u << t) - 1));
+    L.slot_token[slot] = (uint8_t)t;
+    L.slot_w[slot] = sum;
+  }
+  if (lane == 0) L.scratch[32] = __popc(leaders);
 }
 
 // Lists that another kernel has built, as the bytes of lists_at's block; closes with a barrier.
