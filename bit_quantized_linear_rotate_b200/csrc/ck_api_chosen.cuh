@@ -61,6 +61,50 @@ int moe_stages(int offset, int stage, int ctas) {
   return n < 2 ? 0 : std::min(n, ck::moe::kMaxStages);
 }
 
+// Once a device: the kernel may take all of an SM's shared memory, and the SM is set up for that (a CTA
+// of the next kernel can then join one that needs less).
+template <typename Tag, typename KernelT>
+cudaError_t set_smem_all(KernelT kern) {
+  static std::atomic<bool> done[kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+// How many clusters of `cs` CTAs with `smem` bytes run at once: cached a device, kernel, cluster size and
+// KB of shared memory.
+template <typename Tag, typename KernelT>
+int clusters_at_once(KernelT kern, int threads, int smem, int cs) {
+  static std::atomic<int> cache[kMaxDevices][4][256];
+  const int dev = current_device(), slot = cs == 8 ? 3 : cs == 4 ? 2 : cs == 2 ? 1 : 0, kb = (smem + 1023) / 1024;
+  if (dev < 0 || kb >= 256) return 0;
+  int n = cache[dev][slot][kb].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)cs);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = kb * 1024;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = -1;
+    }
+    cache[dev][slot][kb].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 template <typename T, int NT, int KW, bool SELF>
 cudaError_t launch_gate_up(const ck::moe::Maps& maps, const ck::moe::Params& p, cudaStream_t st) {
   using namespace ck::moe;
@@ -76,7 +120,7 @@ cudaError_t launch_gate_up(const ck::moe::Maps& maps, const ck::moe::Params& p, 
   if (stages == 0) return cudaErrorInvalidValue;
   if (SELF) stages = std::min(stages, 3);   // leaves room for a CTA of down_kernel beside it
   const int smem = 1024 + offset + stages * C::kStage;
-  const cudaError_t e = set_smem_max<Tag>(kern, smem, 227 * 1024);
+  const cudaError_t e = set_smem_all<Tag>(kern);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)p.choice.T * p.choice.k * (p.I / kColsItem);   // a unit has a slot at least
   const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)ctas * sm_count());
@@ -90,18 +134,27 @@ cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cud
   auto kern = down_kernel<T, NT, SUB>;
   struct Tag {};
   const int offset = ring_offset(p.choice.T * p.choice.k, C::sums(p.choice.T));
-  const int tiles = p.K / kRowsTile;
-  int ctas = 3;
-  while (ctas > 1 && moe_stages(offset, C::kStage, ctas) == 0) --ctas;
-  int cs = 8;
-  while (cs > 1 && tiles * cs > ctas * sm_count()) cs /= 2;
-  while (ctas > 1 && tiles * cs <= (ctas - 1) * sm_count()) --ctas;   // no more CTAs an SM than there are: deeper rings
-  if (p.lists == nullptr) ctas = 3;                                   // room beside gate_up_kernel's CTA
-  const int stages = moe_stages(offset, C::kStage, ctas);
-  if (stages == 0) return cudaErrorInvalidValue;
-  const int smem = 1024 + offset + stages * C::kStage;
-  const cudaError_t e = set_smem_max<Tag>(kern, smem, 227 * 1024);
+  cudaError_t e = set_smem_all<Tag>(kern);
   if (e != cudaSuccess) return e;
+  // Two CTAs an SM (one where the sums leave no room). The cluster size by the time expected: rounds of
+  // clusters (33 of 8 run at once, 71 of 4), each some 0.5 us a step and 0.35 us a CTA of the cluster for
+  // meeting and adding up (fitted to 1 to 110 steps: a single token is fastest in clusters of 4, 16
+  // tokens of 64 experts in clusters of 8, 51 against 59 us).
+  const int tiles = p.K / kRowsTile;
+  const double units = p.choice.E * (1 - std::pow(1 - std::min(1.0, (double)p.choice.k / p.choice.E), p.choice.T));
+  const double steps = std::max(1.0, units) * ((p.I + 64 * C::kSubs - 1) / (64 * C::kSubs));
+  int ctas = 2, cs = 0;
+  int stages = moe_stages(offset, C::kStage, ctas);
+  if (stages == 0) stages = moe_stages(offset, C::kStage, ctas = 1);
+  const int smem = 1024 + offset + stages * C::kStage;
+  double best = 1e30;
+  for (int s = 1; s <= 8; s *= 2) {
+    const int fit = clusters_at_once<Tag>(kern, C::kThreads, smem, s);
+    if (stages == 0 || fit <= 0) continue;
+    const double t = ((tiles + fit - 1) / fit) * (std::ceil(steps / s) * 0.5 + 0.35 * s);
+    if (t < best) best = t, cs = s;
+  }
+  if (cs == 0) return cudaErrorInvalidValue;
   return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, C::kThreads, smem, st, maps, p, stages);
 }
 

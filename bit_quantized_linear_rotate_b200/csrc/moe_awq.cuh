@@ -182,18 +182,20 @@ __device__ __forceinline__ void mma_u8s8(int (&c)[4], const uint32_t (&a)[4], ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// tot += the sub-block's sum of W x = s (d I - 8 X) + z X, for the tile's rows r and r + 1 and
-// token t of the four in b. dx: {d, X} of that token's block.
-__device__ __forceinline__ void add_block(float (&tot)[2], const uint32_t (&a)[2][4], const uint4 b, const float2 s,
+// Two floats as one operand of a packed instruction.
+__device__ __forceinline__ float2 fma2(const float2 a, const float2 b, const float2 c) { return __ffma2_rn(a, b, c); }
+
+// tot += the sub-block's sum of W x = s (d I - 8 X) + z X, for the tile's rows r and r + 1 (packed: three
+// instructions for six) and token t of the four in b. dx: {d, X} of that token's block.
+__device__ __forceinline__ void add_block(float2& tot, const uint32_t (&a)[2][4], const uint4 b, const float2 s,
                                           const float2 z, const float2 dx) {
   int c[4] = {0, 0, 0, 0};
   mma_u8s8(c, a[0], b.x, b.y);
   mma_u8s8(c, a[1], b.z, b.w);
+  const float2 i2 = make_float2((float)(c[0] * 128 + c[1]), (float)(c[2] * 128 + c[3]));
   const float x8 = -8.0f * dx.y;
-  tot[0] = fmaf(s.x, fmaf(dx.x, (float)(c[0] * 128 + c[1]), x8), tot[0]);
-  tot[1] = fmaf(s.y, fmaf(dx.x, (float)(c[2] * 128 + c[3]), x8), tot[1]);
-  tot[0] = fmaf(z.x, dx.y, tot[0]);
-  tot[1] = fmaf(z.y, dx.y, tot[1]);
+  tot = fma2(s, fma2(make_float2(dx.x, dx.x), i2, make_float2(x8, x8)), tot);
+  tot = fma2(z, make_float2(dx.y, dx.y), tot);
 }
 
 // ------------------------------------------------------------------ the ring
@@ -379,7 +381,7 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
 
   const int kw = warp >> 2, rq = warp & 3;
   Cursor at;
-  float tot[2][NT][2];
+  float2 tot[2][NT];
   // One item's products with N token tiles; sums in tot.
   auto products = [&](auto tiles, int start, int n) {
     constexpr int N = decltype(tiles)::value;
@@ -396,7 +398,7 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int tt = 0; tt < N; ++tt) tot[m][tt][0] = tot[m][tt][1] = 0.0f;
+      for (int tt = 0; tt < N; ++tt) tot[m][tt] = make_float2(0.0f, 0.0f);
     const int r = 16 * rq + 2 * g;
     for (int ch = 0; ch < nchunk; ++ch, at.next(stages)) {
       const uint8_t* st = ring + at.stage * C::kStage;
@@ -432,13 +434,14 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
     const int start = L.unit_start[u], n = L.unit_n[u], nt = (n + 3) >> 2;
     if (NT == 1 || n <= 4) products(std::integral_constant<int, 1>(), start, n);
     else if (NT == 2 || n <= 8) products(std::integral_constant<int, NT < 2 ? 1 : 2>(), start, n);
+    else if (n <= 12) products(std::integral_constant<int, NT < 3 ? 1 : 3>(), start, n);
     else products(std::integral_constant<int, NT>(), start, n);
     if (turn != 0) consumers_sync<32 * C::kCons>();   // the previous item's sums have been read
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int tt = 0; tt < NT; ++tt)
-        if (tt < nt) red[((warp * 2 + m) * NT + tt) * 32 + lane] = make_float2(tot[m][tt][0], tot[m][tt][1]);
+        if (tt < nt) red[((warp * 2 + m) * NT + tt) * 32 + lane] = tot[m][tt];
     consumers_sync<32 * C::kCons>();
     // Token c of the unit: a lane forms columns 2 lane and 2 lane + 1. The other warps go on.
     for (int c = (warp + turn) & (C::kCons - 1); c < n; c += C::kCons) {
@@ -618,7 +621,9 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
         bq[tt] = min(4 * tt + (g >> 1), n - 1) * SUB * kRecord + kw * 128 + (g & 1) * 64 + t * 16;
         bs[tt] = min(4 * tt + t, n - 1) * SUB * kRecord + 512 + kw * 8;
       }
-      float tot[2][N][2] = {};
+      float2 tot[2][N];
+#pragma unroll
+      for (int tt = 0; tt < N; ++tt) tot[0][tt] = tot[1][tt] = make_float2(0.0f, 0.0f);
       for (; chunks > 0; ch += stride, --chunks, at.next(stages)) {
         const uint8_t* st = ring + at.stage * C::kStage;
         const uint8_t* rec = st + C::kW + 2 * C::kS;
@@ -652,8 +657,8 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
         if (i < n) {
           float2* ap = reinterpret_cast<float2*>(acc + L.slot_token[start + i] * kRowsTile);
           const float2 v = ap[0], w = ap[8];
-          ap[0] = make_float2(v.x + tot[0][tt][0], v.y + tot[0][tt][1]);
-          ap[8] = make_float2(w.x + tot[1][tt][0], w.y + tot[1][tt][1]);
+          ap[0] = make_float2(v.x + tot[0][tt].x, v.y + tot[0][tt].y);
+          ap[8] = make_float2(w.x + tot[1][tt].x, w.y + tot[1][tt].y);
         }
       }
       __syncwarp();                                 // another lane may hold this token in the next unit
@@ -663,6 +668,7 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
       const int n = L.unit_n[u];
       if (NT == 1 || n <= 4) products(std::integral_constant<int, 1>(), u, ch, chunks);
       else if (NT == 2 || n <= 8) products(std::integral_constant<int, NT < 2 ? 1 : 2>(), u, ch, chunks);
+      else if (n <= 12) products(std::integral_constant<int, NT < 3 ? 1 : 3>(), u, ch, chunks);
       else products(std::integral_constant<int, NT>(), u, ch, chunks);
       left -= chunks;
     }
