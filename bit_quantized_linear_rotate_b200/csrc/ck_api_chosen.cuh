@@ -127,11 +127,11 @@ cudaError_t launch_gate_up(const ck::moe::Maps& maps, const ck::moe::Params& p, 
   return launch_pdl(kern, dim3(grid), dim3(C::kThreads), smem, st, maps, p, stages);
 }
 
-template <typename T, int NT, int SUB>
+template <typename T, int NT>
 cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cudaStream_t st) {
   using namespace ck::moe;
-  using C = Down<NT, SUB>;
-  auto kern = down_kernel<T, NT, SUB>;
+  using C = Down<NT>;
+  auto kern = down_kernel<T, NT>;
   struct Tag {};
   const int offset = ring_offset(p.choice.T * p.choice.k, C::sums(p.choice.T));
   cudaError_t e = set_smem_all<Tag>(kern);
@@ -189,7 +189,6 @@ int moe_token_tiles(const ck::moe::Params& p) {
   return likely <= 4 ? 1 : likely <= 8 ? 2 : 4;
 }
 int gate_up_stage_cols(const ck::moe::Params& p) { return moe_self(p) ? 512 : 256; }
-int down_stage_cols(const ck::moe::Params& p) { return moe_token_tiles(p) <= 2 ? 512 : 256; }
 
 template <typename T>
 cudaError_t launch_moe(const ck::moe::Maps& gate_up, const ck::moe::Maps& down, ck::moe::Params& p, uint8_t* ws,
@@ -209,9 +208,9 @@ cudaError_t launch_moe(const ck::moe::Maps& gate_up, const ck::moe::Maps& down, 
                    : launch_gate_up<T, 4, 2, false>(gate_up, p, st);
   }
   if (e != cudaSuccess) return e;
-  return tiles == 1 ? launch_down<T, 1, 2>(down, p, st)
-       : tiles == 2 ? launch_down<T, 2, 2>(down, p, st)
-                    : launch_down<T, 4, 1>(down, p, st);
+  return tiles == 1 ? launch_down<T, 1>(down, p, st)
+       : tiles == 2 ? launch_down<T, 2>(down, p, st)
+                    : launch_down<T, 4>(down, p, st);
 }
 
 // Maps of `rows` weight rows of `cols` columns for each expert: boxes of 64
@@ -276,7 +275,7 @@ ck_status moe_impl(const char* who, const MoeArgs& a, const ck::moe::Choice& cho
   Maps gate_up, down;
   ck_status r = make_expert_maps(&gate_up, a.gq, a.gs, a.gz, a.E, 2 * a.I, a.K, a.G, gate_up_stage_cols(p));
   if (r != CK_OK) return r;
-  r = make_expert_maps(&down, a.dq, a.ds, a.dz, a.E, a.K, a.I, a.G, down_stage_cols(p));
+  r = make_expert_maps(&down, a.dq, a.ds, a.dz, a.E, a.K, a.I, a.G, 512);
   if (r != CK_OK) return r;
   const cudaError_t e = a.dt == CK_BF16 ? launch_moe<__nv_bfloat16>(gate_up, down, p, ws, w, st)
                                         : launch_moe<__half>(gate_up, down, p, ws, w, st);

@@ -46,8 +46,8 @@ constexpr int kMaxStages = 6;
 // Rows of activations as fixed point, in records of four sub-blocks: for each of
 // them 128 bytes, the hi bytes of its 64 columns, then the lo bytes, both in four
 // runs of 16 columns in the order 0 2 4 6 1 3 5 7 8 10 12 14 9 11 13 15 (low nibbles of a packed
-// word, then its high nibbles); behind the four, {d, X} of each.
-constexpr int kRecord = 4 * 128 + 4 * 8;
+// word, then its high nibbles); behind the four, {d, d, X, X} of each (operands of packed instructions).
+constexpr int kRecord = 4 * 128 + 4 * 16;
 __host__ __device__ constexpr int row_bytes(int columns) { return (columns + 255) / 256 * kRecord; }
 
 struct Params {
@@ -86,6 +86,8 @@ __device__ __forceinline__ int fixed_point(float v, float inv) {
   return inv == 0.0f ? 0 : __float2int_rn(v * inv);
 }
 
+__device__ __forceinline__ float4 pair_scales(float d, float x) { return make_float4(d, d, x, x); }
+
 // Converts row `row` of x (K values) by a group of THREADS threads (a multiple of 8), 8 columns
 // a thread at a time; lane groups of eight hold a sub-block.
 template <typename T, int THREADS>
@@ -120,7 +122,7 @@ __device__ __forceinline__ void convert_row(const T* x, int K, uint8_t* row, int
       uint8_t* q = rec + (sb & 3) * 128 + part * 8;
       *reinterpret_cast<uint2*>(q) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(q + 64) = make_uint2(lo[0], lo[1]);
-      if (part == 0) reinterpret_cast<float2*>(rec + 512)[sb & 3] = make_float2(d.x, d.x * (float)sum);
+      if (part == 0) reinterpret_cast<float4*>(rec + 512)[sb & 3] = pair_scales(d.x, d.x * (float)sum);
     }
   }
 }
@@ -157,14 +159,17 @@ __device__ __forceinline__ float2 load_pair(const uint8_t* p) {
   return make_float2(awq::Traits<T>::tof(v[0]), awq::Traits<T>::tof(v[1]));
 }
 
-// A tile of 16 weight rows x 64 columns as the A operands of two MMAs, from a
-// box of 256 columns: 16-byte chunk c of row r is at c ^ (r % 8). Row g of the
-// fragment is row r = r0 + 2 g, row g + 8 is r + 1, so that a lane's two
-// scales are neighbours and a half-warp's reads hit each bank once.
-__device__ __forceinline__ void load_tile(const uint8_t* box, int r, int sb, int t, uint32_t (&a)[2][4]) {
-  const int c = 2 * (sb & 3) + (t >> 1), b = 8 * (t & 1);
-  const uint2 w0 = *reinterpret_cast<const uint2*>(box + r * 128 + ((c ^ (r & 7)) << 4) + b);
-  const uint2 w1 = *reinterpret_cast<const uint2*>(box + (r + 1) * 128 + ((c ^ ((r + 1) & 7)) << 4) + b);
+// Where a lane finds its 8 packed bytes of row r (even) and sub-block sb (0 .. 3) in a box of 256
+// columns: 16-byte chunk c of row r is at c ^ (r % 8). Row r + 1's are at (that ^ 16) + 128, and those of
+// sub-block sb ^ 2 at that ^ 64. Row g of an MMA's fragment is row r = r0 + 2 g, row g + 8 is r + 1: a lane's
+// two scales are neighbours, and a half-warp's reads hit each bank once.
+__device__ __forceinline__ int tile_offset(int r, int sb, int t) {
+  return r * 128 + (((2 * sb + (t >> 1)) ^ (r & 7)) << 4) + 8 * (t & 1);
+}
+
+// A tile of 16 weight rows x 64 columns as the A operands of two MMAs: the lane's bytes of rows r and r + 1.
+__device__ __forceinline__ void load_tile(const uint8_t* row0, const uint8_t* row1, uint32_t (&a)[2][4]) {
+  const uint2 w0 = *reinterpret_cast<const uint2*>(row0), w1 = *reinterpret_cast<const uint2*>(row1);
   a[0][0] = w0.x & 0x0F0F0F0Fu;
   a[0][1] = w1.x & 0x0F0F0F0Fu;
   a[0][2] = (w0.x >> 4) & 0x0F0F0F0Fu;
@@ -182,20 +187,16 @@ __device__ __forceinline__ void mma_u8s8(int (&c)[4], const uint32_t (&a)[4], ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two floats as one operand of a packed instruction.
-__device__ __forceinline__ float2 fma2(const float2 a, const float2 b, const float2 c) { return __ffma2_rn(a, b, c); }
-
 // tot += the sub-block's sum of W x = s (d I - 8 X) + z X, for the tile's rows r and r + 1 (packed: three
-// instructions for six) and token t of the four in b. dx: {d, X} of that token's block.
+// instructions for six) and token t of the four in b. dx: that token's {d, d, X, X}, x8: {-8 X, -8 X}.
 __device__ __forceinline__ void add_block(float2& tot, const uint32_t (&a)[2][4], const uint4 b, const float2 s,
-                                          const float2 z, const float2 dx) {
+                                          const float2 z, const float4 dx, const float2 x8) {
   int c[4] = {0, 0, 0, 0};
   mma_u8s8(c, a[0], b.x, b.y);
   mma_u8s8(c, a[1], b.z, b.w);
   const float2 i2 = make_float2((float)(c[0] * 128 + c[1]), (float)(c[2] * 128 + c[3]));
-  const float x8 = -8.0f * dx.y;
-  tot = fma2(s, fma2(make_float2(dx.x, dx.x), i2, make_float2(x8, x8)), tot);
-  tot = fma2(z, make_float2(dx.y, dx.y), tot);
+  tot = __ffma2_rn(s, __ffma2_rn(make_float2(dx.x, dx.y), i2, x8), tot);
+  tot = __ffma2_rn(z, make_float2(dx.z, dx.w), tot);
 }
 
 // ------------------------------------------------------------------ the ring
@@ -285,7 +286,7 @@ constexpr int kSelfBytes = 32 * 1024;
 template <int NT, int KW, bool SELF>
 struct GateUp {
   static constexpr int kCons = 4 * KW, kThreads = 32 * (kCons + 1);
-  static constexpr int kCtas = KW == 2 ? 3 : 1;                 // on an SM
+  static constexpr int kCtas = KW == 4 ? 1 : 2;     // on an SM (three with shallower rings: 49 against 46.5 us at 16 tokens)
   static constexpr int kSubs = 2 * KW;                          // sub-blocks a stage
   static constexpr int kW = kSubs * 64 * 32;                    // its bytes of gate (or up) weights
   static constexpr int kS = kSubs * 128;                        // bytes of each kind of scales
@@ -380,6 +381,8 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
   }
 
   const int kw = warp >> 2, rq = warp & 3;
+  const int tile = tile_offset(16 * rq + 2 * g, kw, t);
+  const int sc0 = (kw >> p.gsh) * 128 + 32 * rq + 4 * g, sc1 = ((kw + KW) >> p.gsh) * 128 + 32 * rq + 4 * g;
   Cursor at;
   float2 tot[2][NT];
   // One item's products with N token tiles; sums in tot.
@@ -392,14 +395,13 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
     for (int tt = 0; tt < N; ++tt) {
       const int c = min(4 * tt + (g >> 1), n - 1), d = min(4 * tt + t, n - 1);
       const int rows = SELF ? xrow : (C::kSubs / 4) * kRecord;
-      bq[tt] = (SELF ? L.slot_token[start + c] : c) * rows + (g & 1) * 64 + t * 16;
-      bs[tt] = (SELF ? L.slot_token[start + d] : d) * rows + 512;
+      bq[tt] = (SELF ? L.slot_token[start + c] : c) * rows + kw * 128 + (g & 1) * 64 + t * 16;
+      bs[tt] = (SELF ? L.slot_token[start + d] : d) * rows + 512 + kw * 16;
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int tt = 0; tt < N; ++tt) tot[m][tt] = make_float2(0.0f, 0.0f);
-    const int r = 16 * rq + 2 * g;
     for (int ch = 0; ch < nchunk; ++ch, at.next(stages)) {
       const uint8_t* st = ring + at.stage * C::kStage;
       const uint8_t* rec = SELF ? own + ch * (C::kSubs / 4) * kRecord : st + 2 * C::kW + 4 * C::kS;
@@ -408,21 +410,26 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
       for (int i = 0; i < 2; ++i) {
         const int sb = kw + KW * i;      // of the stage
         if (C::kSubs * ch + sb >= nsub) break;
+        // KW = 2: sub-blocks kw and kw + 2 of one box; KW = 4: sub-block kw of two boxes
+        const uint8_t* row0 = st + (KW == 2 && i == 1 ? tile ^ 64 : tile) + (KW == 4 ? i * 64 * 128 : 0);
+        const uint8_t* row1 = st + 128 + (KW == 2 && i == 1 ? tile ^ 80 : tile ^ 16) + (KW == 4 ? i * 64 * 128 : 0);
+        const uint8_t* sp = st + 2 * C::kW + (i == 0 ? sc0 : sc1);
         uint4 b[N];
-        float2 dx[N];
+        float4 dx[N];
+        float2 x8[N];
 #pragma unroll
         for (int tt = 0; tt < N; ++tt) {
-          b[tt] = *reinterpret_cast<const uint4*>(rec + bq[tt] + (sb >> 2) * kRecord + (sb & 3) * 128);
-          dx[tt] = *reinterpret_cast<const float2*>(rec + bs[tt] + (sb >> 2) * kRecord + (sb & 3) * 8);
+          b[tt] = *reinterpret_cast<const uint4*>(rec + bq[tt] + (KW == 4 ? i * kRecord : i * 256));
+          dx[tt] = *reinterpret_cast<const float4*>(rec + bs[tt] + (KW == 4 ? i * kRecord : i * 32));
+          x8[tt] = __fmul2_rn(make_float2(-8.0f, -8.0f), make_float2(dx[tt].z, dx[tt].w));
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {    // gate, up
           uint32_t a[2][4];
-          load_tile(st + m * C::kW + (sb >> 2) * 64 * 128, r, sb, t, a);
-          const uint8_t* sp = st + 2 * C::kW + 2 * m * C::kS + (sb >> p.gsh) * 128 + 2 * r;
-          const float2 s = load_pair<T>(sp), z = load_pair<T>(sp + C::kS);
+          load_tile(row0 + m * C::kW, row1 + m * C::kW, a);
+          const float2 s = load_pair<T>(sp + 2 * m * C::kS), z = load_pair<T>(sp + 2 * m * C::kS + C::kS);
 #pragma unroll
-          for (int tt = 0; tt < N; ++tt) add_block(tot[m][tt], a, b[tt], s, z, dx[tt]);
+          for (int tt = 0; tt < N; ++tt) add_block(tot[m][tt], a, b[tt], s, z, dx[tt], x8[tt]);
         }
       }
       ring_release(R, at);
@@ -468,7 +475,7 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
       q[68] = (uint8_t)(f1 - 128 * a1);
       if (lane == 0) {                   // with the token's weight: down_kernel only adds
         const float w = L.slot_w[start + c];
-        reinterpret_cast<float2*>(rec + 512)[cb & 3] = make_float2(w * d.x, w * (d.x * (float)sum));
+        reinterpret_cast<float4*>(rec + 512)[cb & 3] = pair_scales(w * d.x, w * (d.x * (float)sum));
       }
     }
   }
@@ -490,14 +497,15 @@ __global__ void __maxnreg__(64)
 
 // --------------------------------------------------------------------- down
 
-// A cluster of CTAs owns 64 output columns and walks (unit, 256 SUB columns of h)
+// A cluster of CTAs owns 64 output columns and walks (unit, 512 columns of h)
 // steps, each CTA a share of them; consumer warp (kw, rh) takes sub-blocks
-// kw (and kw + 4) of a step and 32 of the output columns. When the unit changes, each warp
+// kw and kw + 4 of a step and 32 of the output columns. When the unit changes, each warp
 // adds its sums to the accumulator (T, 64) that it shares with the other rh; at the
 // end the four accumulators and then the CTAs' are added in order. The weights of
 // the first stages are fetched before the dependency wait, the rows of h after it.
-template <int NT, int SUB>
+template <int NT>
 struct Down {
+  static constexpr int SUB = 2;                  // sub-blocks a warp and step (1: 20 us slower at 32 tokens, 8 wide experts)
   static constexpr int kCons = 8, kThreads = 32 * (kCons + 1);
   static constexpr int kSubs = 4 * SUB;
   static constexpr int kW = kSubs * 64 * 32;
@@ -506,10 +514,11 @@ struct Down {
   __host__ __device__ static constexpr int sums(int T) { return 4 * T * kRowsTile * 4; }
 };
 
-template <typename T, int NT, int SUB>
-__global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
+template <typename T, int NT>
+__global__ void __launch_bounds__(Down<NT>::kThreads, 2)
     down_kernel(const __grid_constant__ Maps maps, const Params p, int stages) {
-  using C = Down<NT, SUB>;
+  using C = Down<NT>;
+  constexpr int SUB = C::SUB;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = align_1024(sm_raw);
   Ring& R = *reinterpret_cast<Ring*>(sm);
@@ -610,6 +619,8 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
     grid_dep_launch();
     const int kw = warp >> 1, rh = warp & 1;
     float* acc = sums + kw * cells + 32 * rh + 2 * g;
+    const int tile = tile_offset(32 * rh + 2 * g, kw, t);
+    const int sc0 = (kw >> p.gsh) * 128 + 64 * rh + 4 * g, sc1 = ((kw + 4) >> p.gsh) * 128 + 64 * rh + 4 * g;
     Cursor at;
     // `chunks` steps of unit u from chunk ch on, with N token tiles.
     auto products = [&](auto tiles, int u, int ch, int chunks) {
@@ -619,7 +630,7 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
 #pragma unroll
       for (int tt = 0; tt < N; ++tt) {
         bq[tt] = min(4 * tt + (g >> 1), n - 1) * SUB * kRecord + kw * 128 + (g & 1) * 64 + t * 16;
-        bs[tt] = min(4 * tt + t, n - 1) * SUB * kRecord + 512 + kw * 8;
+        bs[tt] = min(4 * tt + t, n - 1) * SUB * kRecord + 512 + kw * 16;
       }
       float2 tot[2][N];
 #pragma unroll
@@ -632,21 +643,24 @@ __global__ void __launch_bounds__(Down<NT, SUB>::kThreads, 3)
         for (int i = 0; i < SUB; ++i) {
           if (C::kSubs * ch + kw + 4 * i >= nsub) break;
           uint4 b[N];
-          float2 dx[N];
+          float4 dx[N];
+          float2 x8[N];
 #pragma unroll
           for (int tt = 0; tt < N; ++tt) {
             b[tt] = *reinterpret_cast<const uint4*>(rec + bq[tt] + i * kRecord);
-            dx[tt] = *reinterpret_cast<const float2*>(rec + bs[tt] + i * kRecord);
+            dx[tt] = *reinterpret_cast<const float4*>(rec + bs[tt] + i * kRecord);
+            x8[tt] = __fmul2_rn(make_float2(-8.0f, -8.0f), make_float2(dx[tt].z, dx[tt].w));
           }
+          const uint8_t* row0 = st + tile + i * 64 * 128;
+          const uint8_t* row1 = st + 128 + (tile ^ 16) + i * 64 * 128;
+          const uint8_t* sp = st + C::kW + (i == 0 ? sc0 : sc1);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            const int r = 32 * rh + 16 * m + 2 * g;
             uint32_t a[2][4];
-            load_tile(st + i * 64 * 128, r, kw, t, a);
-            const uint8_t* sp = st + C::kW + ((kw + 4 * i) >> p.gsh) * 128 + 2 * r;
-            const float2 sc = load_pair<T>(sp), z = load_pair<T>(sp + C::kS);
+            load_tile(row0 + m * 16 * 128, row1 + m * 16 * 128, a);
+            const float2 sc = load_pair<T>(sp + 32 * m), z = load_pair<T>(sp + 32 * m + C::kS);
 #pragma unroll
-            for (int tt = 0; tt < N; ++tt) add_block(tot[m][tt], a, b[tt], sc, z, dx[tt]);
+            for (int tt = 0; tt < N; ++tt) add_block(tot[m][tt], a, b[tt], sc, z, dx[tt], x8[tt]);
           }
         }
         ring_release(R, at);

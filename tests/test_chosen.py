@@ -187,8 +187,8 @@ def test_moe_choice_validation(ck):
     assert moe_call(ck, True, ids=None) == 1
     assert moe_call(ck, True, w=None) == 1
     assert moe_call(ck, True, w=P((1 << 20) + 2)) == 1
-    # x and h in records of 544 bytes for 256 columns, the lists: each rounded up to 256 bytes
-    assert ck.moe_awq_w4a16_workspace_bytes(4, 2, 320, 64) == 17 * 256 + 17 * 256 + 256
+    # x and h in records of 576 bytes for 256 columns, the lists: each rounded up to 256 bytes
+    assert ck.moe_awq_w4a16_workspace_bytes(4, 2, 320, 64) == 18 * 256 + 18 * 256 + 256
     assert ck.moe_awq_w4a16_workspace_bytes(0, 2, 128, 64) == 0
 
 
