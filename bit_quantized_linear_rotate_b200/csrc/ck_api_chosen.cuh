@@ -285,17 +285,28 @@ ck_status moe_impl(const char* who, const MoeArgs& a, const ck::moe::Choice& cho
 
 // ----------------------------------------------------------------- adapters
 
-template <typename T, typename TY, int RC, int TM>
-cudaError_t launch_lora_tm(const ck::lora::Params& p, int64_t tiles, cudaStream_t st) {
+template <typename T, typename TY, int RC>
+cudaError_t launch_lora_few(const ck::lora::Params& p, int64_t tiles, cudaStream_t st) {
   using namespace ck::lora;
-  auto kern = lora_kernel<T, TY, RC, TM>;
-  using SM = Smem<RC, TM>;
+  auto kern = lora_kernel<T, TY, RC>;
   struct Tag {};
-  const cudaError_t e = set_smem_max<Tag>(kern, (int)sizeof(SM), (int)sizeof(SM));
+  const int smem = (int)sizeof(Smem<RC>);
+  const cudaError_t e = set_smem_max<Tag>(kern, smem, smem);
   if (e != cudaSuccess) return e;
-  int cs = 8;
-  while (cs > 1 && tiles * cs > 2 * sm_count() && TM > 16) cs /= 2;
-  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kThreads, sizeof(SM), st, p);
+  // The cluster size by the time expected: rounds of as many clusters as run at once, each a share of a tile's
+  // adapter (at 14 GB/s a CTA) and some 4 us for finding the tile and exchanging v; the number of
+  // tiles, known on the device only, as that of the different ids that M draws make.
+  const double work = 2.0 * p.R * ((double)p.K + p.N) / 14e3;
+  const double likely = std::max(1.0, (p.L + 1) * (1 - std::pow(1 - 1.0 / (p.L + 1), p.M)) + (double)p.M / kFewTile / 2);
+  int cs = 1;
+  double best = 1e30;
+  for (int s = 8; s >= 1; s /= 2) {
+    const int fit = clusters_at_once<Tag>(kern, kThreads, smem, s);
+    if (fit <= 0) continue;
+    const double t = std::ceil(std::min(likely, (double)tiles) / fit) * (work / s + 4);
+    if (t < best) best = t, cs = s;
+  }
+  return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, kThreads, smem, st, p);
 }
 
 template <typename T, typename TY, int RB>
@@ -336,17 +347,18 @@ cudaError_t launch_lora_tc(const ck::lora::Params& p, int64_t tiles, cudaStream_
 
 template <typename T, typename TY>
 cudaError_t launch_lora(const ck::lora::Params& p, int tm, int64_t tiles, cudaStream_t st) {
-  if (tm == 16) {
-    if (p.R <= 32) return launch_lora_tm<T, TY, 1, 16>(p, tiles, st);
-    if (p.R <= 64) return launch_lora_tm<T, TY, 2, 16>(p, tiles, st);
-    return launch_lora_tm<T, TY, 4, 16>(p, tiles, st);
+  using ck::lora::kFewTile;
+  if (tm == kFewTile) {
+    if (p.R <= 32) return launch_lora_few<T, TY, 1>(p, tiles, st);
+    if (p.R <= 64) return launch_lora_few<T, TY, 2>(p, tiles, st);
+    return launch_lora_few<T, TY, 4>(p, tiles, st);
   }
   return p.R <= 64 ? launch_lora_tc<T, TY, 1>(p, tiles, st) : launch_lora_tc<T, TY, 2>(p, tiles, st);
 }
 
 // Tokens of a tile, by how many tokens an adapter has on average.
 int lora_tile(int64_t M, int64_t L) {
-  return M > ck::lora::kSelfGroup && M >= 32 * L ? ck::lora::kTcTokens : 16;
+  return M > ck::lora::kSelfGroup && M >= 32 * L ? ck::lora::kTcTokens : ck::lora::kFewTile;
 }
 
 // Whether the CTAs find their tiles themselves; else group_kernel lists them.

@@ -3,7 +3,7 @@
 //   out[m, :] = y[m, :] + scale[a] * ((x[m, :] A[a]^T) B[a]^T),   a = ids[m]
 //   out[m, :] = y[m, :]                                           where a is no adapter
 //
-// A tile is at most TM tokens of one adapter. A cluster of CTAs computes it in
+// A tile is at most 16 tokens of one adapter. A cluster of CTAs computes it in
 // one launch: each CTA multiplies its share of K (v = x A^T, the "shrink"), the
 // partial v are added through distributed shared memory in rank order, and
 // each CTA then multiplies all of v with its share of B's N rows and adds y (the
@@ -346,34 +346,36 @@ __device__ __forceinline__ void copy_rows(const TY* y, TY* out, const Params& p,
   }
 }
 
-// Shared memory of a CTA: RC 32-wide chunks of rank, TM tokens.
-template <int RC, int TM>
-struct Smem {
+// Shared memory of a CTA: RC 32-wide chunks of rank.
+constexpr int kFewTile = 16;                          // tokens of a tile
+template <int RC>
+struct alignas(16) Smem {
   static constexpr int kR = 32 * RC;
   static constexpr int kVStride = kR + 8;             // 16-bit elements: rows 16 bytes apart in the banks
-  static constexpr int kSplit = kWarps / (TM / 16);   // warps that share an m16 tile in the shrink
-  float part[kSplit][TM][kR];                         // the warps' sums; [0]: this CTA's
-  float v[TM][kR];                                    // the cluster's
-  uint16_t hi[TM][kVStride], lo[TM][kVStride];
-  float row_scale[TM];
-  int token[TM];
+  float part[kWarps][kFewTile][kR];                         // the warps' sums; [0]: this CTA's
+  float v[kFewTile][kR];                                    // the cluster's
+  uint16_t hi[kFewTile][kVStride], lo[kFewTile][kVStride];
+  float row_scale[kFewTile];
+  int token[kFewTile];
   int scratch[kSelfGroup + 16];
 };
 
-template <typename T, typename TY, int RC, int TM>
-__global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
+// Many small CTAs hide each other's latencies (ranks up to 32: three an SM). Bringing B into shared memory from
+// the start took their place on the SMs: 29 us for a decode step of 64 tokens that takes 20 so.
+template <typename T, typename TY, int RC>
+__global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t sm[];
-  using SM = Smem<RC, TM>;
+  using SM = Smem<RC>;
   using Tr = awq::Traits<T>;
   SM& S = *reinterpret_cast<SM*>(sm);
-  constexpr int MT = TM / 16, KS = SM::kSplit, RT = 4 * RC;
+  constexpr int RT = 4 * RC;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
   grid_dep_wait();
   grid_dep_launch();
   int adapter;
-  const int n = find_tile<TM>(p, (int)(blockIdx.x / ranks), S.token, adapter, S.scratch);
+  const int n = find_tile<kFewTile>(p, (int)(blockIdx.x / ranks), S.token, adapter, S.scratch);
   if (n == 0) return;                                 // the same for all CTAs of the cluster
   const T* x = reinterpret_cast<const T*>(p.x);
   const TY* y = reinterpret_cast<const TY*>(p.y);
@@ -385,65 +387,70 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     copy_rows(y, out, p, S.token, n, 32 * nb0, min(32 * nb1, p.N), warp, kWarps);
     return;
   }
+  const T* b = reinterpret_cast<const T*>(p.b) + ((int64_t)adapter * p.N + 32 * nb0) * p.R;   // this CTA's share
 
   // ---- shrink: part = x A^T over this warp's share of k
   {
-    const int mt = warp % MT, ks = warp / MT;
     const int nk = (p.K + 31) / 32;
-    const int kc0 = (int)((int64_t)nk * (rank * KS + ks) / (ranks * KS));
-    const int kc1 = (int)((int64_t)nk * (rank * KS + ks + 1) / (ranks * KS));
-    const int m0 = 16 * mt + g, m1 = m0 + 8;
-    const T* x0 = m0 < n ? x + S.token[m0] * p.ldx + 8 * t : nullptr;
-    const T* x1 = m1 < n ? x + S.token[m1] * p.ldx + 8 * t : nullptr;
+    const int kc0 = (int)((int64_t)nk * (rank * kWarps + warp) / (ranks * kWarps));
+    const int kc1 = (int)((int64_t)nk * (rank * kWarps + warp + 1) / (ranks * kWarps));
+    const T* x0 = g < n ? x + S.token[g] * p.ldx + 8 * t : nullptr;
+    const T* x1 = g + 8 < n ? x + S.token[g + 8] * p.ldx + 8 * t : nullptr;
     const T* ap = reinterpret_cast<const T*>(p.a) + ((int64_t)adapter * p.R + g) * p.K + 8 * t;
     float c[RT][4] = {};
-    if (16 * mt < n) {
 #pragma unroll 2
-      for (int kc = kc0; kc < kc1; ++kc) {
-        const int k = 32 * kc;
-        const bool in = k + 8 * t < p.K;              // K % 8 == 0: all eight or none
-        uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;
-        if (in && x0 != nullptr) q0 = *reinterpret_cast<const uint4*>(x0 + k);
-        if (in && x1 != nullptr) q1 = *reinterpret_cast<const uint4*>(x1 + k);
-        const uint32_t fa[4] = {q0.x, q1.x, q0.y, q1.y}, fb[4] = {q0.z, q1.z, q0.w, q1.w};
+    for (int kc = kc0; kc < kc1; ++kc) {
+      const int k = 32 * kc;
+      const bool in = k + 8 * t < p.K;                // K % 8 == 0: all eight or none
+      uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;
+      if (in && x0 != nullptr) q0 = *reinterpret_cast<const uint4*>(x0 + k);
+      if (in && x1 != nullptr) q1 = *reinterpret_cast<const uint4*>(x1 + k);
+      const uint32_t fa[4] = {q0.x, q1.x, q0.y, q1.y}, fb[4] = {q0.z, q1.z, q0.w, q1.w};
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          if (8 * j >= p.R) break;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (in) w = __ldg(reinterpret_cast<const uint4*>(ap + (int64_t)8 * j * p.K + k));
-          Tr::mma(c[j], fa, w.x, w.y);
-          Tr::mma(c[j], fb, w.z, w.w);
-        }
+      for (int j = 0; j < RT; ++j) {
+        if (8 * j >= p.R) break;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (in) w = __ldg(reinterpret_cast<const uint4*>(ap + (int64_t)8 * j * p.K + k));
+        Tr::mma(c[j], fa, w.x, w.y);
+        Tr::mma(c[j], fb, w.z, w.w);
       }
     }
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      *reinterpret_cast<float2*>(&S.part[ks][m0][8 * j + 2 * t]) = make_float2(c[j][0], c[j][1]);
-      *reinterpret_cast<float2*>(&S.part[ks][m1][8 * j + 2 * t]) = make_float2(c[j][2], c[j][3]);
+      *reinterpret_cast<float2*>(&S.part[warp][g][8 * j + 2 * t]) = make_float2(c[j][0], c[j][1]);
+      *reinterpret_cast<float2*>(&S.part[warp][g + 8][8 * j + 2 * t]) = make_float2(c[j][2], c[j][3]);
     }
   }
   __syncthreads();
-  constexpr int kCells = TM * SM::kR;
-  float* part = &S.part[0][0][0];
+  constexpr int kCells = kFewTile * SM::kR / 4;             // of four floats
+  float4* part = reinterpret_cast<float4*>(&S.part[0][0][0]);
   for (int i = tid; i < kCells; i += kThreads) {
-    float s = part[i];
+    float4 s = part[i];
 #pragma unroll
-    for (int w = 1; w < KS; ++w) s += part[w * kCells + i];
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 u = part[w * kCells + i];
+      s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+    }
     part[i] = s;
   }
   // each CTA adds its share of the cells over the ranks and hands the sums to all
   cluster_sync();
   const uint32_t part_at = smem_u32(part), v_at = smem_u32(&S.v[0][0]);
-  for (int i = rank * kThreads + tid; i < kCells; i += ranks * kThreads) {
-    float s = 0.0f;
-    for (int r = 0; r < ranks; ++r) s += ld_cluster_f32(mapa_shared(part_at + 4 * i, r));
-    for (int r = 0; r < ranks; ++r) st_cluster_f32(mapa_shared(v_at + 4 * i, r), s);
+  for (int i = tid * ranks + rank; i < kCells; i += ranks * kThreads) {
+    float4 u[8], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if (r < ranks) u[r] = ld_cluster_f32x4(mapa_shared(part_at + 16 * i, r));
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if (r < ranks) s.x += u[r].x, s.y += u[r].y, s.z += u[r].z, s.w += u[r].w;
+    for (int r = 0; r < ranks; ++r) st_cluster_f32x4(mapa_shared(v_at + 16 * i, r), s);
   }
   cluster_sync();
 
   // ---- v as hi + lo
   const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
-  for (int m = warp; m < TM; m += kWarps) {
+  for (int m = warp; m < kFewTile; m += kWarps) {
     float v[RC];
     int ex = 0;
 #pragma unroll
@@ -467,61 +474,54 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
   __syncthreads();
 
   // ---- expand: out = y + row_scale * (v B^T), 32 columns at a time
-  const T* b = reinterpret_cast<const T*>(p.b) + (int64_t)adapter * p.N * p.R + 8 * t;
-  for (int blk = nb0 + warp; blk < nb1; blk += kWarps) {
-    const int c0 = 32 * blk;
-    float c[MT][4][4] = {};
+  using TrY = awq::Traits<TY>;
+  for (int blk = warp; blk < nb1 - nb0; blk += kWarps) {
+    const int c0 = 32 * (nb0 + blk), col = c0 + 8 * t;   // the lane's eight columns: col ..
+    float c[4][4] = {};
 #pragma unroll
     for (int rc = 0; rc < RC; ++rc) {
       if (32 * rc >= p.R) break;
       uint4 w[4];
+      const int at = 32 * rc + 8 * t;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int col = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
+        const int row = 32 * blk + 8 * (g >> 1) + 2 * j + (g & 1);      // of this CTA's share
         w[j] = make_uint4(0, 0, 0, 0);
-        if (col < p.N && 32 * rc + 8 * t < p.R) w[j] = __ldg(reinterpret_cast<const uint4*>(b + (int64_t)col * p.R + 32 * rc));
+        if (32 * nb0 + row < p.N && at < p.R)
+          w[j] = __ldg(reinterpret_cast<const uint4*>(b + (int64_t)row * p.R + at));
       }
+      const uint4 h0 = *reinterpret_cast<const uint4*>(&S.hi[g][at]), h1 = *reinterpret_cast<const uint4*>(&S.hi[g + 8][at]);
+      const uint4 l0 = *reinterpret_cast<const uint4*>(&S.lo[g][at]), l1 = *reinterpret_cast<const uint4*>(&S.lo[g + 8][at]);
+      const uint32_t ha[4] = {h0.x, h1.x, h0.y, h1.y}, hb[4] = {h0.z, h1.z, h0.w, h1.w};
+      const uint32_t la[4] = {l0.x, l1.x, l0.y, l1.y}, lb[4] = {l0.z, l1.z, l0.w, l1.w};
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (16 * mt >= n) break;
-        const int m0 = 16 * mt + g, at = 32 * rc + 8 * t;
-        const uint4 h0 = *reinterpret_cast<const uint4*>(&S.hi[m0][at]), h1 = *reinterpret_cast<const uint4*>(&S.hi[m0 + 8][at]);
-        const uint4 l0 = *reinterpret_cast<const uint4*>(&S.lo[m0][at]), l1 = *reinterpret_cast<const uint4*>(&S.lo[m0 + 8][at]);
-        const uint32_t ha[4] = {h0.x, h1.x, h0.y, h1.y}, hb[4] = {h0.z, h1.z, h0.w, h1.w};
-        const uint32_t la[4] = {l0.x, l1.x, l0.y, l1.y}, lb[4] = {l0.z, l1.z, l0.w, l1.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          Tr::mma(c[mt][j], ha, w[j].x, w[j].y);
-          Tr::mma(c[mt][j], hb, w[j].z, w[j].w);
-          Tr::mma(c[mt][j], la, w[j].x, w[j].y);
-          Tr::mma(c[mt][j], lb, w[j].z, w[j].w);
-        }
+      for (int j = 0; j < 4; ++j) {
+        Tr::mma(c[j], ha, w[j].x, w[j].y);
+        Tr::mma(c[j], hb, w[j].z, w[j].w);
+        Tr::mma(c[j], la, w[j].x, w[j].y);
+        Tr::mma(c[j], lb, w[j].z, w[j].w);
       }
     }
-    using TrY = awq::Traits<TY>;
-    const int col = c0 + 8 * t;                       // this lane's eight columns
+    if (col >= p.N) continue;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int hf = 0; hf < 2; ++hf) {
+      const int m = g + 8 * hf;
+      if (m >= n) continue;
+      const float f = S.row_scale[m];
+      const TY* yp = y + S.token[m] * p.ldy + col;
+      TY* op = out + S.token[m] * p.ldo + col;
+      if (p.vec) {
+        uint4 u = *reinterpret_cast<const uint4*>(yp);
+        TY* e = reinterpret_cast<TY*>(&u);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int m = 16 * mt + g + 8 * hf;
-        if (m >= n || col >= p.N) continue;
-        const float f = S.row_scale[m];
-        const TY* yp = y + S.token[m] * p.ldy + col;
-        TY* op = out + S.token[m] * p.ldo + col;
-        TY e[8];
-        if (p.vec) {
-          *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(yp);
+        for (int i = 0; i < 8; ++i) e[i] = TrY::fromf(fmaf(f, c[i >> 1][2 * hf + (i & 1)], TrY::tof(e[i])));
+        *reinterpret_cast<uint4*>(op) = u;
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            e[i] = TrY::fromf(fmaf(f, c[mt][i >> 1][2 * hf + (i & 1)], TrY::tof(e[i])));
-          *reinterpret_cast<uint4*>(op) = *reinterpret_cast<const uint4*>(e);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col + i < p.N) op[i] = TrY::fromf(fmaf(f, c[mt][i >> 1][2 * hf + (i & 1)], TrY::tof(yp[i])));
-        }
+        for (int i = 0; i < 8; ++i)
+          if (col + i < p.N) op[i] = TrY::fromf(fmaf(f, c[i >> 1][2 * hf + (i & 1)], TrY::tof(yp[i])));
       }
+    }
   }
 }
 
