@@ -10,6 +10,7 @@ libck.so raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -448,7 +449,11 @@ def gemv_awq_w4a16(x, qweight, wscales, wzeros, bias=None, group_size: int = 64,
 # ------------------------------------------ weights chosen for each token
 #
 # These calls are short (some 5 us on the device), so their checks are one expression over cheap
-# attributes; only when it fails does a slower function find out what is wrong and say so.
+# attributes; only where it fails does a slower function find out what is wrong and say so (or that the
+# call is merely less usual).
+
+_moe_bytes = functools.lru_cache(maxsize=1024)(lib.ck_moe_awq_w4a16_workspace_bytes)
+_lora_bytes = functools.lru_cache(maxsize=1024)(lib.ck_lora_add_workspace_bytes)
 
 _LOGITS = (torch.bfloat16, torch.float16, torch.float32)
 _f32t, _i32t, _bf16t = torch.float32, torch.int32, torch.bfloat16
@@ -559,25 +564,26 @@ def _moe(fn, name, x, given, choice, top_k, gate_up_q, gate_up_s, gate_up_z, dow
     G = int(group_size)
     dt = x.dtype
     dev = x.get_device()
-    fast = (x.dim() == 2 and gate_up_q.dim() == 3 and G > 0 and dt in _HALF and gate_up_s.dtype == dt
-            and gate_up_z.dtype == dt and down_s.dtype == dt and down_z.dtype == dt and gate_up_q.dtype in _byte_like
-            and down_q.dtype in _byte_like and workspace is None and out is None)
-    if fast:
-        T, K = x.shape
-        E, I = gate_up_q.shape[0], gate_up_q.shape[1] >> 1
-        Kh, Kg, Ig = K >> 1, K // G, I // G
-        fast = (gate_up_q.shape == (E, 2 * I, Kh) and gate_up_s.shape == (E, Kg, 2 * I)
-                and gate_up_z.shape == gate_up_s.shape and down_q.shape == (E, K, I >> 1)
-                and down_s.shape == (E, Ig, K) and down_z.shape == down_s.shape and gate_up_q.is_contiguous() and gate_up_s.is_contiguous()
-                and gate_up_z.is_contiguous() and down_q.is_contiguous() and down_s.is_contiguous()
-                and down_z.is_contiguous() and (x.stride(1) == 1 or K <= 1)
+    try:
+        (T, K), (E, rows, half), (Ed, Kd, Ih) = x.shape, gate_up_q.shape, down_q.shape
+        I = rows >> 1
+        fine = (G > 0 and half == K >> 1 and rows == 2 * I and Ed == E and Kd == K and Ih == I >> 1
+                and gate_up_s.shape == (E, K // G, rows) and gate_up_z.shape == gate_up_s.shape
+                and down_s.shape == (E, I // G, K) and down_z.shape == down_s.shape and dt in _HALF
+                and gate_up_s.dtype == dt and gate_up_z.dtype == dt and down_s.dtype == dt and down_z.dtype == dt
+                and gate_up_q.dtype in _byte_like and down_q.dtype in _byte_like and gate_up_q.is_contiguous()
+                and gate_up_s.is_contiguous() and gate_up_z.is_contiguous() and down_q.is_contiguous()
+                and down_s.is_contiguous() and down_z.is_contiguous() and x.is_contiguous()
+                and workspace is None and out is None
                 and _on(dev, *given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z))
-    if not fast:
+    except ValueError:                            # another number of dimensions
+        fine = False
+    if not fine:
         _no_moe(name, x, given, gate_up_q, gate_up_s, gate_up_z, down_q, down_s, down_z, G, workspace, out)
-        T, K = x.shape
-        E, I = gate_up_q.shape[0], gate_up_q.shape[1] >> 1
+        (T, K), (E, rows) = x.shape, gate_up_q.shape[:2]
+        I = rows >> 1
     if workspace is None:
-        workspace = _empty(x, (int(lib.ck_moe_awq_w4a16_workspace_bytes(T, top_k, K, I)),), torch.uint8, stream)
+        workspace = _empty(x, (_moe_bytes(T, top_k, K, I),), torch.uint8, stream)
     if out is None:
         out = _empty(x, (T, K), dt, stream)
     _run(fn, name, dev, stream, x.data_ptr(), 0 if dt == _bf16t else 1, T, K, I, E, x.stride(0) if T > 1 else K, G,
@@ -650,22 +656,25 @@ def lora_add(y, x, lora_a, lora_b, ids, scales=None, workspace=None, out=None, s
     (L, N, R) are the adapters, ids (M,) int32 (-1: none), scales (L,) float32. `out` may be y: in place."""
     dt, ydt = x.dtype, y.dtype
     dev = x.get_device()
-    if not (x.dim() == 2 and lora_a.dim() == 3 and lora_b.dim() == 3 and dt in _HALF and lora_a.dtype == dt
-            and lora_b.dtype == dt and (ydt == dt or ydt == _bf16t) and ids.dtype == _i32t
-            and ids.shape == x.shape[:1] and ids.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous()
-            and lora_a.shape[2] == x.shape[1] and lora_b.shape[0] == lora_a.shape[0]
-            and lora_b.shape[2] == lora_a.shape[1] and y.shape == (x.shape[0], lora_b.shape[1])
-            and x.is_contiguous() and y.is_contiguous() and workspace is None and (out is None or out is y)
-            and (scales is None or (scales.dtype == _f32t and scales.shape == lora_a.shape[:1]
-                                    and scales.is_contiguous()))
-            and _on(dev, y, lora_a, lora_b, ids, scales)):
+    try:
+        (M, K), (L, R, Ka), (Lb, N, Rb), (My, Ny), (Mi,) = x.shape, lora_a.shape, lora_b.shape, y.shape, ids.shape
+        fine = (Ka == K and Lb == L and Rb == R and My == M and Ny == N and Mi == M and dt in _HALF
+                and lora_a.dtype == dt and lora_b.dtype == dt and (ydt == dt or ydt == _bf16t) and ids.dtype == _i32t
+                and x.is_contiguous() and y.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous()
+                and ids.is_contiguous() and workspace is None and (out is None or out is y) and dev >= 0
+                and y.get_device() == dev and lora_a.get_device() == dev and lora_b.get_device() == dev
+                and ids.get_device() == dev
+                and (scales is None or (scales.dtype == _f32t and scales.shape == (L,) and scales.is_contiguous()
+                                        and scales.get_device() == dev)))
+    except ValueError:                            # another number of dimensions
+        fine = False
+    if not fine:
         _no_lora(y, x, lora_a, lora_b, ids, scales, workspace, out)
-    M, K = x.shape
-    L, N, R = lora_b.shape
+        (M, K), (L, N, R) = x.shape, lora_b.shape
     if out is None:
         out = _empty(y, (M, N), ydt, stream)
     if workspace is None:
-        need = lib.ck_lora_add_workspace_bytes(M, L)
+        need = _lora_bytes(M, L)
         if need:
             workspace = _empty(x, (need,), torch.uint8, stream)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), _nbytes(workspace))
