@@ -76,32 +76,34 @@ cudaError_t set_smem_all(KernelT kern) {
   return e;
 }
 
-// How many clusters of `cs` CTAs with `smem` bytes run at once: cached a device, kernel, cluster size and
-// KB of shared memory.
+// How many clusters of `cs` CTAs with `smem` bytes run at once (0: none). Remembered for each kernel and
+// device in a small table; an entry holds its key and the answer.
 template <typename Tag, typename KernelT>
 int clusters_at_once(KernelT kern, int threads, int smem, int cs) {
-  static std::atomic<int> cache[kMaxDevices][4][256];
-  const int dev = current_device(), slot = cs == 8 ? 3 : cs == 4 ? 2 : cs == 2 ? 1 : 0, kb = (smem + 1023) / 1024;
-  if (dev < 0 || kb >= 256) return 0;
-  int n = cache[dev][slot][kb].load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cs;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)cs);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = kb * 1024;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
-      cudaGetLastError();
-      n = -1;
-    }
-    cache[dev][slot][kb].store(n, std::memory_order_relaxed);
+  static std::atomic<uint64_t> table[kMaxDevices][64];
+  const int dev = current_device(), kb = (smem + 1023) / 1024;
+  if (dev < 0) return 0;
+  const uint32_t key = (uint32_t)(kb * 16 + cs);
+  std::atomic<uint64_t>& entry = table[dev][(kb * 4 + (cs == 8 ? 3 : cs == 4 ? 2 : cs - 1)) & 63];
+  const uint64_t known = entry.load(std::memory_order_relaxed);
+  if ((uint32_t)(known >> 32) == key) return (int)(uint32_t)known;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)cs);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 0) {
+    cudaGetLastError();
+    n = 0;
   }
+  entry.store((uint64_t)key << 32 | (uint32_t)n, std::memory_order_relaxed);
   return n;
 }
 
