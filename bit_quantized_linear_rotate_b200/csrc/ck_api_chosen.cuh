@@ -177,13 +177,18 @@ struct MoeWorkspace {
   }
 };
 
-// Which kernels a call runs. Up to 4 tokens: 16 consumer warps, one CTA an SM, which routes and
-// converts x itself. Else three CTAs an SM, and token tiles (of four) a unit by how many
+// Which kernels a call runs. One or two tokens whose items (64 columns of h of an expert) each get
+// an SM of their own: 16 consumer warps, one CTA an SM, which routes and converts x itself (K = 2048,
+// top-8 of 64, I = 1024: 14.2 us for one token, 16.0 with prepare_kernel). With a second
+// round of items it loses: the same at two tokens 23.6 against 22.1 us, and K = 4096, I = 4096,
+// top-4 at one 31.8 against 28.4; three and four tokens lose up to 9 us and win 1 at K = 1024.
+// Else two CTAs an SM, and token tiles (of four) a unit by how many
 // tokens an expert is likely to get, the mean and three standard deviations: an expert with
 // more is read again for the rest, while room for 16 tokens in every stage costs depth of the ring.
 bool moe_self(const ck::moe::Params& p) {
-  return p.choice.T <= ck::moe::kFewTokens && p.choice.T * p.choice.k <= ck::moe::kFewSlots &&
-         p.choice.T * ck::moe::row_bytes(p.K) <= ck::moe::kSelfBytes;
+  const int64_t items = (int64_t)p.choice.T * p.choice.k * (p.I / ck::moe::kColsItem);
+  return p.choice.T <= ck::moe::kFewTokens && items <= sm_count() &&
+         p.choice.T * p.choice.k <= ck::moe::kFewSlots && p.choice.T * ck::moe::row_bytes(p.K) <= ck::moe::kSelfBytes;
 }
 int moe_token_tiles(const ck::moe::Params& p) {
   const double mean = (double)p.choice.T * p.choice.k / p.choice.E;

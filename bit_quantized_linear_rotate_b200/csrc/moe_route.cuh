@@ -238,11 +238,11 @@ __device__ __forceinline__ void build_lists(const Choice& c, const Lists& L, Lis
   __syncthreads();
 }
 
-// The same for at most 32 slots of at most four tokens, by warp 0, a slot a lane, from the choice in
+// The same for at most 32 slots of at most two tokens, by warp 0, a slot a lane, from the choice in
 // tmp (choose_few and a barrier before it). An expert is one unit (cap >= 4), in the order in
 // which the slots first name them. Every CTA of both kernels of a small batch builds them
 // (3.3 us by build_lists, most of it barriers and waits on shared memory; 0.3 so).
-constexpr int kFewTokens = 4, kFewSlots = 32;
+constexpr int kFewTokens = 2, kFewSlots = 32;
 struct FewTemp {
   float w[kFewSlots];
   int id[kFewSlots];
@@ -277,7 +277,7 @@ __device__ __forceinline__ void list_few(const Choice& c, const Lists& L, const 
   const float w = in ? tmp.w[lane] : 0.0f;
   const bool live = e >= 0;
   const unsigned same = __match_any_sync(kAll, live ? e : -1 - lane);            // slots of this expert
-  const unsigned twin = __match_any_sync(kAll, live ? 4 * e + t : -1 - lane);    // of this expert and token
+  const unsigned twin = __match_any_sync(kAll, live ? kFewTokens * e + t : -1 - lane);    // of this expert and token
   float sum = 0.0f;                                  // the twins' weights, in order
   for (unsigned left = __reduce_or_sync(kAll, __popc(twin) > 1 ? twin : 0u); left != 0; left &= left - 1) {
     const int j = __ffs(left) - 1;

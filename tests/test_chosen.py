@@ -371,11 +371,12 @@ def test_moe_given_choice_with_empty_and_repeated_slots(on_gpu, dtype):
 @gpu
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_moe_given_choice_of_few_tokens(on_gpu, dtype):
-    # the same in the kernels for up to four tokens
+    # the same for one and two tokens, which route in every block, and for the lists of three and four
     E, K, I = 7, 320, 192
     gu, dn = experts(E, K, I, 64, dtype, 4)
     g = torch.Generator().manual_seed(4)
-    for rows in ([[2, 2, 2, 2]], [[-1, -1, 9, -5]], [[6, 0, 6, 1], [1, 1, 0, -1], [-1, -1, -1, -1], [0, 6, 1, 1]],
+    for rows in ([[2, 2, 2, 2]], [[-1, -1, 9, -5]], [[6, 0, 6, 1], [1, 1, 0, -1]], [[0, 0, 0], [-1, -1, -1]],
+                 [[4], [4]], [[1, 2, 3, 4, 5, 6, 0, 1, 1, 1], [6, 6, 0, 5, 4, 3, 2, 1, 0, 0]], [[6, 0, 6, 1], [1, 1, 0, -1], [-1, -1, -1, -1], [0, 6, 1, 1]],
                  [[3], [3], [3], [3]], [[1, 2, 3, 4, 5, 6, 0, 1, 1, 1]] * 3):
         ids = torch.tensor(rows, dtype=torch.int32)
         w = torch.randn(ids.shape, generator=g)
@@ -386,7 +387,7 @@ def test_moe_given_choice_of_few_tokens(on_gpu, dtype):
 
 
 @gpu
-@pytest.mark.parametrize("T", [1, 4, 16])
+@pytest.mark.parametrize("T", [1, 2, 4, 16])
 def test_moe_equals_route_and_given_experts_bit_for_bit(on_gpu, T):
     E, k, K, I = 32, 6, 512, 256
     gu, dn = experts(E, K, I, 64, BF, 1)
@@ -423,6 +424,11 @@ def test_moe_tokens_do_not_depend_on_their_neighbours(on_gpu):
     masked[5] = -float("inf")                               # a padded row: no expert
     got = on_gpu.moe_awq_w4a16(x, masked, k, *gu, *dn)
     assert not got[5].any()
+    pair = on_gpu.moe_awq_w4a16(bad[2:4], logits[2:4], k, *gu, *dn)
+    assert torch.equal(pair[0], on_gpu.moe_awq_w4a16(x[2:4], logits[2:4], k, *gu, *dn)[0])
+    assert not torch.isfinite(pair[1]).any()
+    pair = on_gpu.moe_awq_w4a16(x[4:6], masked[4:6], k, *gu, *dn)
+    assert pair[0].any() and not pair[1].any()
 
 
 @gpu
