@@ -360,10 +360,13 @@ struct alignas(16) Smem {
   int scratch[kSelfGroup + 16];
 };
 
-// Many small CTAs hide each other's latencies (ranks up to 32: three an SM). Bringing B into shared memory from
-// the start took their place on the SMs: 29 us for a decode step of 64 tokens that takes 20 so.
+// Many small CTAs hide each other's latencies (ranks up to 32: three an SM). Latency bounds them: the loads
+// of a step are all issued before its first product, those of y before those of B (a
+// decode step of 64 tokens, K = 4096, N = 12288, R = 32, 48 adapters 16.7 us, 20.0 with a load
+// for each product; one token, K = N = 4096, R = 128 10.4, 18.1 so). Bringing B into shared
+// memory from the start took the place of CTAs on the SMs: 29 us for that decode step.
 template <typename T, typename TY, int RC>
-__global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : RC == 2 ? 2 : 1) lora_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t sm[];
   using SM = Smem<RC>;
   using Tr = awq::Traits<T>;
@@ -398,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
     const T* x1 = g + 8 < n ? x + S.token[g + 8] * p.ldx + 8 * t : nullptr;
     const T* ap = reinterpret_cast<const T*>(p.a) + ((int64_t)adapter * p.R + g) * p.K + 8 * t;
     float c[RT][4] = {};
-#pragma unroll 2
+    constexpr int kBatch = RT < 8 ? RT : 8;           // loads of A at once
+#pragma unroll 1
     for (int kc = kc0; kc < kc1; ++kc) {
       const int k = 32 * kc;
       const bool in = k + 8 * t < p.K;                // K % 8 == 0: all eight or none
@@ -407,12 +411,20 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
       if (in && x1 != nullptr) q1 = *reinterpret_cast<const uint4*>(x1 + k);
       const uint32_t fa[4] = {q0.x, q1.x, q0.y, q1.y}, fb[4] = {q0.z, q1.z, q0.w, q1.w};
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        if (8 * j >= p.R) break;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (in) w = __ldg(reinterpret_cast<const uint4*>(ap + (int64_t)8 * j * p.K + k));
-        Tr::mma(c[j], fa, w.x, w.y);
-        Tr::mma(c[j], fb, w.z, w.w);
+      for (int j0 = 0; j0 < RT; j0 += kBatch) {
+        if (8 * j0 >= p.R) break;
+        uint4 w[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          w[j] = make_uint4(0, 0, 0, 0);
+          if (in && 8 * (j0 + j) < p.R)
+            w[j] = __ldg(reinterpret_cast<const uint4*>(ap + (int64_t)8 * (j0 + j) * p.K + k));
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          Tr::mma(c[j0 + j], fa, w[j].x, w[j].y);
+          Tr::mma(c[j0 + j], fb, w[j].z, w[j].w);
+        }
       }
     }
 #pragma unroll
@@ -423,8 +435,9 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
   }
   __syncthreads();
   constexpr int kCells = kFewTile * SM::kR / 4;             // of four floats
+  const int cells = n * SM::kR / 4;                         // of this tile's tokens: other rows of v are not used
   float4* part = reinterpret_cast<float4*>(&S.part[0][0][0]);
-  for (int i = tid; i < kCells; i += kThreads) {
+  for (int i = tid; i < cells; i += kThreads) {
     float4 s = part[i];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
   // each CTA adds its share of the cells over the ranks and hands the sums to all
   cluster_sync();
   const uint32_t part_at = smem_u32(part), v_at = smem_u32(&S.v[0][0]);
-  for (int i = tid * ranks + rank; i < kCells; i += ranks * kThreads) {
+  for (int i = tid * ranks + rank; i < cells; i += ranks * kThreads) {
     float4 u[8], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int r = 0; r < 8; ++r)
@@ -450,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
 
   // ---- v as hi + lo
   const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
-  for (int m = warp; m < kFewTile; m += kWarps) {
+  for (int m = warp; m < n; m += kWarps) {
     float v[RC];
     int ex = 0;
 #pragma unroll
@@ -478,28 +491,41 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
   for (int blk = warp; blk < nb1 - nb0; blk += kWarps) {
     const int c0 = 32 * (nb0 + blk), col = c0 + 8 * t;   // the lane's eight columns: col ..
     float c[4][4] = {};
+    uint4 yq[2] = {};
 #pragma unroll
-    for (int rc = 0; rc < RC; ++rc) {
-      if (32 * rc >= p.R) break;
-      uint4 w[4];
-      const int at = 32 * rc + 8 * t;
+    for (int hf = 0; hf < 2; ++hf)
+      if (p.vec && col < p.N && g + 8 * hf < n)
+        yq[hf] = *reinterpret_cast<const uint4*>(y + S.token[g + 8 * hf] * p.ldy + col);
+    constexpr int kBatch = RC < 2 ? RC : 2;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = 32 * blk + 8 * (g >> 1) + 2 * j + (g & 1);      // of this CTA's share
-        w[j] = make_uint4(0, 0, 0, 0);
-        if (32 * nb0 + row < p.N && at < p.R)
-          w[j] = __ldg(reinterpret_cast<const uint4*>(b + (int64_t)row * p.R + at));
-      }
-      const uint4 h0 = *reinterpret_cast<const uint4*>(&S.hi[g][at]), h1 = *reinterpret_cast<const uint4*>(&S.hi[g + 8][at]);
-      const uint4 l0 = *reinterpret_cast<const uint4*>(&S.lo[g][at]), l1 = *reinterpret_cast<const uint4*>(&S.lo[g + 8][at]);
-      const uint32_t ha[4] = {h0.x, h1.x, h0.y, h1.y}, hb[4] = {h0.z, h1.z, h0.w, h1.w};
-      const uint32_t la[4] = {l0.x, l1.x, l0.y, l1.y}, lb[4] = {l0.z, l1.z, l0.w, l1.w};
+    for (int r0 = 0; r0 < RC; r0 += kBatch) {
+      if (32 * r0 >= p.R) break;
+      uint4 w[kBatch][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        Tr::mma(c[j], ha, w[j].x, w[j].y);
-        Tr::mma(c[j], hb, w[j].z, w[j].w);
-        Tr::mma(c[j], la, w[j].x, w[j].y);
-        Tr::mma(c[j], lb, w[j].z, w[j].w);
+      for (int rc = 0; rc < kBatch; ++rc)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = 32 * blk + 8 * (g >> 1) + 2 * j + (g & 1);      // of this CTA's share
+          const int at = 32 * (r0 + rc) + 8 * t;
+          w[rc][j] = make_uint4(0, 0, 0, 0);
+          if (32 * nb0 + row < p.N && at < p.R)
+            w[rc][j] = __ldg(reinterpret_cast<const uint4*>(b + (int64_t)row * p.R + at));
+        }
+#pragma unroll
+      for (int rc = 0; rc < kBatch; ++rc) {
+        if (32 * (r0 + rc) >= p.R) break;
+        const int at = 32 * (r0 + rc) + 8 * t;
+        const uint4 h0 = *reinterpret_cast<const uint4*>(&S.hi[g][at]), h1 = *reinterpret_cast<const uint4*>(&S.hi[g + 8][at]);
+        const uint4 l0 = *reinterpret_cast<const uint4*>(&S.lo[g][at]), l1 = *reinterpret_cast<const uint4*>(&S.lo[g + 8][at]);
+        const uint32_t ha[4] = {h0.x, h1.x, h0.y, h1.y}, hb[4] = {h0.z, h1.z, h0.w, h1.w};
+        const uint32_t la[4] = {l0.x, l1.x, l0.y, l1.y}, lb[4] = {l0.z, l1.z, l0.w, l1.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          Tr::mma(c[j], ha, w[rc][j].x, w[rc][j].y);
+          Tr::mma(c[j], hb, w[rc][j].z, w[rc][j].w);
+          Tr::mma(c[j], la, w[rc][j].x, w[rc][j].y);
+          Tr::mma(c[j], lb, w[rc][j].z, w[rc][j].w);
+        }
       }
     }
     if (col >= p.N) continue;
@@ -511,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
       const TY* yp = y + S.token[m] * p.ldy + col;
       TY* op = out + S.token[m] * p.ldo + col;
       if (p.vec) {
-        uint4 u = *reinterpret_cast<const uint4*>(yp);
+        uint4 u = yq[hf];
         TY* e = reinterpret_cast<TY*>(&u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = TrY::fromf(fmaf(f, c[i >> 1][2 * hf + (i & 1)], TrY::tof(e[i])));
