@@ -140,8 +140,10 @@ cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cud
   if (e != cudaSuccess) return e;
   // Two CTAs an SM (one where the sums leave no room). The cluster size by the time expected: rounds of
   // clusters (33 of 8 run at once, 71 of 4), each some 0.5 us a step and 0.35 us a CTA of the cluster for
-  // meeting and adding up (fitted to 1 to 110 steps: a single token is fastest in clusters of 4, 16
-  // tokens of 64 experts in clusters of 8, 51 against 59 us).
+  // meeting and adding up (fitted to 1 to 110 steps: 16 tokens of 64 experts, K = 2048, are fastest in
+  // clusters of 8, 47.5 against 57.8 us in clusters of 4; 32 tokens of 16 experts, K = 5120, of 3, 76
+  // against 87 in clusters of 2). Behind gate_up_few_kernel, beside which there is room for one CTA an
+  // SM, every CTA costs (K = 3840, one token: 17.4 us in clusters of 2, 19.3 of 4).
   const int tiles = p.K / kRowsTile;
   const double units = p.choice.E * (1 - std::pow(1 - std::min(1.0, (double)p.choice.k / p.choice.E), p.choice.T));
   const double steps = std::max(1.0, units) * ((p.I + 64 * C::kSubs - 1) / (64 * C::kSubs));
@@ -150,10 +152,11 @@ cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cud
   if (stages == 0) stages = moe_stages(offset, C::kStage, ctas = 1);
   const int smem = 1024 + offset + stages * C::kStage;
   double best = 1e30;
-  for (int s = 1; s <= 8; s *= 2) {
+  const double each = p.lists == nullptr ? 0.012 : 0.0;
+  for (int s = 1; s <= 8; ++s) {
     const int fit = clusters_at_once<Tag>(kern, C::kThreads, smem, s);
     if (stages == 0 || fit <= 0) continue;
-    const double t = ((tiles + fit - 1) / fit) * (std::ceil(steps / s) * 0.5 + 0.35 * s);
+    const double t = ((tiles + fit - 1) / fit) * (std::ceil(steps / s) * 0.5 + 0.35 * s) + each * tiles * s;
     if (t < best) best = t, cs = s;
   }
   if (cs == 0) return cudaErrorInvalidValue;
