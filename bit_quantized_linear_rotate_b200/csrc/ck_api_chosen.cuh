@@ -343,11 +343,13 @@ cudaError_t launch_lora_tc(const ck::lora::Params& p, int64_t tiles, cudaStream_
     return cudaErrorInvalidValue;
   // The cluster size by the time it is expected to take: rounds of as many clusters as run at once (15 of
   // 8 CTAs, 22 of 6), each 1 / cs of a tile's bytes (at an SM's 43 GB/s) and 6 us for the stages that
-  // wait for one another; the number of tiles, known on the device only, as that of as many tokens
-  // for every adapter and for none (M = 2048, K = N = 4096, R = 16, 4 adapters: 24.7 us with clusters of 6,
-  // 36.8 with clusters of 8, the best if all SMs took part).
+  // wait for one another (M = 2048, K = N = 4096, R = 16, 4 adapters: 24.7 us with clusters of 6, 36.8 with
+  // clusters of 8, the best if all SMs took part). The number of tiles, known on the device only, is taken
+  // between that of requests of 128 tokens, each with any adapter or none, and that of all adapters in turn.
   const double work = 128.0 * (p.K + 2.0 * p.N) * 2 / 43e3, fixed = 6.0;
-  const double likely = (p.L + 1) * std::max(1.0, (double)p.M / (p.L + 1) / kTcTokens + 0.5);
+  const double full = (double)p.M / kTcTokens, ids = p.L + 1.0;
+  auto tiles_of = [&](double adapters) { return adapters * std::max(1.0, full / adapters + 0.5); };
+  const double likely = (tiles_of(ids) + tiles_of(ids * (1 - std::pow(1 - 1 / ids, full)))) / 2;
   int cs = 0;
   double best = 1e30;
   for (int c = 1; c <= 8; ++c) {
