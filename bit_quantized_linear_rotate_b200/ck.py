@@ -585,7 +585,7 @@ def _moe(fn, name, x, given, choice, top_k, gate_up_q, gate_up_s, gate_up_z, dow
     if workspace is None:
         workspace = _empty(x, (_moe_bytes(T, top_k, K, I),), torch.uint8, stream)
     if out is None:
-        out = _empty(x, (T, K), dt, stream)
+        out = torch.empty_like(x) if fine and stream is None else _empty(x, (T, K), dt, stream)
     _run(fn, name, dev, stream, x.data_ptr(), 0 if dt == _bf16t else 1, T, K, I, E, x.stride(0) if T > 1 else K, G,
          *choice, gate_up_q.data_ptr(), gate_up_s.data_ptr(), gate_up_z.data_ptr(), down_q.data_ptr(),
          down_s.data_ptr(), down_z.data_ptr(), out.data_ptr(), workspace.data_ptr(), _nbytes(workspace))
@@ -672,7 +672,7 @@ def lora_add(y, x, lora_a, lora_b, ids, scales=None, workspace=None, out=None, s
         _no_lora(y, x, lora_a, lora_b, ids, scales, workspace, out)
         (M, K), (L, N, R) = x.shape, lora_b.shape
     if out is None:
-        out = _empty(y, (M, N), ydt, stream)
+        out = torch.empty_like(y) if fine and stream is None else _empty(y, (M, N), ydt, stream)
     if workspace is None:
         need = _lora_bytes(M, L)
         if need:
