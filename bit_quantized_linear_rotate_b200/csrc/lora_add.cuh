@@ -38,7 +38,8 @@ namespace lora {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSelfGroup = 256;        // up to this many tokens a cluster finds its tile itself
+constexpr int kSelfGroup = 256;        // up to this many tokens a cluster of few tokens finds its tile itself,
+constexpr int kSelfPick = 4096;        // or this many of at most kPickAdapters adapters (pick_tile)
 constexpr int kMaxAdapters = 8192;     // group_kernel counts them in shared memory
 constexpr int kGroupThreads = 1024;
 
@@ -266,6 +267,14 @@ __device__ __forceinline__ int find_tile(const Params& p, int tile, int (&token)
     __syncthreads();
     return v.z;
   }
+  if (p.M > kSelfGroup) {                             // (pick_tile from 64 tokens on: 1 us slower at 128)
+    int n = 0;
+    for (int i = tid; i < p.L + 1 + 32; i += kThreads) scratch[i] = 0;
+    __syncthreads();
+    pick_tile<kThreads, TM>(p, tile, token, adapter, n, scratch);
+    __syncthreads();
+    return n;
+  }
   // M <= 256 = kThreads: token i's rank among the tokens of its adapter; every TM-th begins a
   // tile, and tiles are numbered by their first tokens.
   int* id = scratch;                                  // [kSelfGroup]
@@ -297,6 +306,8 @@ __device__ __forceinline__ int find_tile(const Params& p, int tile, int (&token)
   adapter = fa;
   return __syncthreads_count(mine);
 }
+
+static_assert(kSelfGroup + 16 <= kPickBytes / 4, "find_tile's scratch");
 
 template <typename T> struct Half2Of;
 template <> struct Half2Of<__nv_bfloat16> { static constexpr bool kScaled = false; };
@@ -357,16 +368,17 @@ struct alignas(16) Smem {
   uint16_t hi[kFewTile][kVStride], lo[kFewTile][kVStride];
   float row_scale[kFewTile];
   int token[kFewTile];
-  int scratch[kSelfGroup + 16];
+  int scratch[kPickBytes / 4];
 };
 
-// Many small CTAs hide each other's latencies (ranks up to 32: three an SM). Latency bounds them: the loads
-// of a step are all issued before its first product, those of y before those of B (a
-// decode step of 64 tokens, K = 4096, N = 12288, R = 32, 48 adapters 16.7 us, 20.0 with a load
-// for each product; one token, K = N = 4096, R = 128 10.4, 18.1 so). Bringing B into shared
-// memory from the start took the place of CTAs on the SMs: 29 us for that decode step.
+// Many small CTAs hide each other's latencies (ranks up to 32: three an SM, else two; 64 tokens with adapters of
+// rank 128, K = N = 4096: 27.4 us, 32.5 with one). Latency bounds them: several loads of a step are
+// issued before its first product, those of y before those of B (a decode step of 64 tokens, K = 4096,
+// N = 12288, R = 32, 48 adapters 16.7 us, 20.0 with a load for each product; its bytes take 6.3 at
+// the measured copy bandwidth). Bringing B into shared memory from the start took the place
+// of CTAs on the SMs: 29 us for that decode step.
 template <typename T, typename TY, int RC>
-__global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : RC == 2 ? 2 : 1) lora_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t sm[];
   using SM = Smem<RC>;
   using Tr = awq::Traits<T>;
@@ -401,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : RC == 2 ? 2 : 1) lora_
     const T* x1 = g + 8 < n ? x + S.token[g + 8] * p.ldx + 8 * t : nullptr;
     const T* ap = reinterpret_cast<const T*>(p.a) + ((int64_t)adapter * p.R + g) * p.K + 8 * t;
     float c[RT][4] = {};
-    constexpr int kBatch = RT < 8 ? RT : 8;           // loads of A at once
+    constexpr int kBatch = RC == 2 ? 8 : 4;           // loads of A at once (RC = 4: 8 leave registers for one CTA an SM)
 #pragma unroll 1
     for (int kc = kc0; kc < kc1; ++kc) {
       const int k = 32 * kc;

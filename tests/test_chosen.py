@@ -211,8 +211,8 @@ def lora_call(ck, **kw):
     (dict(ids=P((1 << 25) + 2)), 1), (dict(s=P((1 << 25) + 2)), 1), (dict(out=P((1 << 20) + 1)), 1),
     (dict(out=P((1 << 20) + 16)), 1),                      # overlaps y without being y
     (dict(ldo=48), 1), (dict(out=P((1 << 24) + 16)), 1),   # over x
-    (dict(M=257, L=9), 1), (dict(M=257, L=9, ws=P(1 << 26), bytes=64), 1),
-    (dict(M=257, L=9, ws=P((1 << 26) + 16), bytes=1 << 20), 1),
+    (dict(M=257, L=2000), 1), (dict(M=257, L=2000, ws=P(1 << 26), bytes=64), 1),
+    (dict(M=257, L=2000, ws=P((1 << 26) + 16), bytes=1 << 20), 1),
     (dict(M=0, y=None, x=None, a=None, b=None, ids=None, out=None), 0)])
 def test_lora_validation(ck, kw, status):
     assert lora_call(ck, **kw) == status
@@ -220,9 +220,9 @@ def test_lora_validation(ck, kw, status):
 
 
 def test_lora_workspace_bytes(ck):
-    for M, L in ((1, 1), (256, 100), (257, 1), (777, 5), (32768, 1024)):
+    for M, L in ((1, 1), (256, 8192), (257, 1), (257, 9), (777, 5), (4096, 1024), (32768, 1024)):
         assert ck.lora_add_workspace_bytes(M, L) == 0       # every CTA finds its tile itself
-    for M, L in ((257, 9), (32769, 1), (32768, 1025), (300, 8192)):
+    for M, L in ((4097, 1024), (32769, 1), (32768, 1025), (257, 1025), (300, 8192)):
         n = ck.lora_add_workspace_bytes(M, L)
         assert n >= 4 * M + 16 * (M // 128 + min(L, 1))     # the token order, and 16 bytes a tile
 
@@ -511,7 +511,8 @@ def test_moe_graph_replay_streams_and_a_shared_workspace(on_gpu):
     (64, 512, 320, 40, 48, 1), (200, 136, 72, 64, 3, 70), (256, 128, 96, 128, 300, 1), (257, 128, 96, 72, 2, 50),
     (513, 200, 129, 16, 3, 100), (777, 1480, 1001, 24, 5, 150), (1030, 96, 256, 128, 4, 1), (600, 64, 64, 8, 2000, 1),
     (2100, 320, 200, 64, 7, 333), (300, 8, 40, 8, 1, 300), (1000, 64, 520, 48, 2, 1), (1500, 1000, 392, 112, 3, 400),
-    (400, 200, 130, 56, 2, 64), (33000, 16, 24, 8, 2, 700), (9000, 24, 16, 16, 200, 3), (20000, 16, 40, 16, 300, 77)])
+    (400, 200, 130, 56, 2, 64), (33000, 16, 24, 8, 2, 700), (9000, 24, 16, 16, 200, 3), (20000, 16, 40, 16, 300, 77),
+    (4096, 16, 24, 8, 1000, 1), (4097, 8, 24, 8, 500, 2), (512, 136, 264, 16, 1, 1), (300, 64, 520, 96, 100, 1)])
 def test_lora(on_gpu, M, K, N, R, L, runs, dtype, ydtype):
     x, y, a, b, ids, scales = adapters(M, K, N, R, L, dtype, ydtype, M + R, runs)
     args = [t.to(DEV) for t in (y, x, a, b, ids)]
@@ -615,7 +616,7 @@ def test_lora_token_does_not_depend_on_its_tile(on_gpu, M):
 
 
 @gpu
-@pytest.mark.parametrize("M,L", [(5, 4), (700, 4), (300, 40)])
+@pytest.mark.parametrize("M,L", [(5, 4), (700, 4), (300, 40), (300, 1100), (5000, 500)])
 def test_lora_graph_replay_streams_and_empty(on_gpu, M, L):
     K, N, R = 128, 64, 16
     x, y, a, b, ids, scales = [t.to(DEV) for t in adapters(M, K, N, R, L, BF, BF, 6)]
