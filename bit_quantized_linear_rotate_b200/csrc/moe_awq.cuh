@@ -53,6 +53,7 @@ constexpr int kMaxStages = 6;
 // runs of 16 columns in the order 0 2 4 6 1 3 5 7 8 10 12 14 9 11 13 15 (low nibbles of a packed
 // word, then its high nibbles); behind the four, {d, d, X, X} of each (operands of packed instructions).
 constexpr int kRecord = 4 * 128 + 4 * 16;
+constexpr int kRowPad = 16;            // between tokens in shared memory: four tokens' scales in different banks
 __host__ __device__ constexpr int row_bytes(int columns) { return (columns + 255) / 256 * kRecord; }
 
 struct Params {
@@ -295,7 +296,8 @@ struct GateUp {
   static constexpr int kSubs = 2 * KW;                          // sub-blocks a stage
   static constexpr int kW = kSubs * 64 * 32;                    // its bytes of gate (or up) weights
   static constexpr int kS = kSubs * 128;                        // bytes of each kind of scales
-  static constexpr int kRows = SELF ? 0 : 4 * NT * (kSubs / 4) * kRecord;
+  static constexpr int kRow = (kSubs / 4) * kRecord + kRowPad;  // of a token's columns of x in a stage
+  static constexpr int kRows = SELF ? 0 : 4 * NT * kRow;
   static constexpr int kStage = (2 * kW + 4 * kS + kRows + 1023) / 1024 * 1024;
   static constexpr int kRed = KW * 4 * 2 * NT * 32 * 8;         // float2 [kw][rq][gate, up][token tile][lane]
   static_assert(sizeof(FewTemp) <= kRed, "the choice is handed on in it");
@@ -377,7 +379,7 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
         }
         __syncwarp();
         if (!SELF && lane < n)
-          bulk_load(st + 2 * C::kW + 4 * C::kS + lane * (C::kSubs / 4) * kRecord, xr + ch * (C::kSubs / 4) * kRecord,
+          bulk_load(st + 2 * C::kW + 4 * C::kS + lane * C::kRow, xr + ch * (C::kSubs / 4) * kRecord,
                     boxes * kRecord, bar);
       }
     }
@@ -399,7 +401,7 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
 #pragma unroll
     for (int tt = 0; tt < N; ++tt) {
       const int c = min(4 * tt + (g >> 1), n - 1), d = min(4 * tt + t, n - 1);
-      const int rows = SELF ? xrow : (C::kSubs / 4) * kRecord;
+      const int rows = SELF ? xrow : C::kRow;
       bq[tt] = (SELF ? L.slot_token[start + c] : c) * rows + kw * 128 + (g & 1) * 64 + t * 16;
       bs[tt] = (SELF ? L.slot_token[start + d] : d) * rows + 512 + kw * 16;
     }
@@ -515,7 +517,8 @@ struct Down {
   static constexpr int kSubs = 4 * SUB;
   static constexpr int kW = kSubs * 64 * 32;
   static constexpr int kS = kSubs * 128;
-  static constexpr int kStage = (kW + 2 * kS + 4 * NT * SUB * kRecord + 1023) / 1024 * 1024;
+  static constexpr int kRow = SUB * kRecord + kRowPad;
+  static constexpr int kStage = (kW + 2 * kS + 4 * NT * kRow + 1023) / 1024 * 1024;
   __host__ __device__ static constexpr int sums(int T) { return 4 * T * kRowsTile * 4; }
 };
 
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(Down<NT>::kThreads, 2)
     auto fetch_rows = [&](int u, int ch, const Cursor& at) {
       const int boxes = min(SUB, (nsub - C::kSubs * ch + 3) >> 2);
       if (lane < L.unit_n[u])
-        bulk_load(ring + at.stage * C::kStage + C::kW + 2 * C::kS + lane * SUB * kRecord,
+        bulk_load(ring + at.stage * C::kStage + C::kW + 2 * C::kS + lane * C::kRow,
                   p.hq + (int64_t)(L.unit_start[u] + lane) * hrow + ch * SUB * kRecord, boxes * kRecord,
                   &R.full[at.stage]);
     };
@@ -634,8 +637,8 @@ __global__ void __launch_bounds__(Down<NT>::kThreads, 2)
       int bq[N], bs[N];
 #pragma unroll
       for (int tt = 0; tt < N; ++tt) {
-        bq[tt] = min(4 * tt + (g >> 1), n - 1) * SUB * kRecord + kw * 128 + (g & 1) * 64 + t * 16;
-        bs[tt] = min(4 * tt + t, n - 1) * SUB * kRecord + 512 + kw * 16;
+        bq[tt] = min(4 * tt + (g >> 1), n - 1) * C::kRow + kw * 128 + (g & 1) * 64 + t * 16;
+        bs[tt] = min(4 * tt + t, n - 1) * C::kRow + 512 + kw * 16;
       }
       float2 tot[2][N];
 #pragma unroll
