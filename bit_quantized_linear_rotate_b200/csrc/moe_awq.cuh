@@ -11,8 +11,8 @@
 // bounds the layer: a tile of 16 weight rows x 64 columns (512 packed bytes) takes one of
 // an SM's four schedulers 89 clocks at the measured copy bandwidth, so a tile must cost well
 // under 89 issue slots. Measured, device time and the bytes' time at the copy bandwidth: 16 tokens, top-8
-// of 64 experts, K = 2048, I = 1024 46.5 us (31.0); 32 tokens, top-2 of 8, K = 3840, I = 10240
-// 143 (77.8), there bound by the latency of the consumers' steps (without the products
+// of 64 experts, K = 2048, I = 1024 45.9 us (31.0); 32 tokens, top-2 of 8, K = 3840, I = 10240
+// 138 (77.8), there bound by the latency of the consumers' steps (without the products
 // the same loads take 100); one token 14.2 (4.4), bound by three dependent phases: the choice, then
 // the weights of gate and up, then those of down.
 //
@@ -133,25 +133,24 @@ __device__ __forceinline__ void convert_row(const T* x, int K, uint8_t* row, int
   }
 }
 
-// ----------------------------------------------------------- prepare (T > 4)
+// ----------------------------------------------------------- prepare
 
-constexpr int kPrepThreads = 512;
 
 // CTA t < T: token t's row of x as fixed point. CTA T: the choice and its lists.
-template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Params p, int cap) {
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS) prepare_kernel(const Params p, int cap) {
   __shared__ ListsTemp tmp;
   __shared__ __align__(16) uint8_t block[lists_bytes(kMaxSlots)];
   grid_dep_wait();
   grid_dep_launch();
   const int t = blockIdx.x, slots = p.choice.T * p.choice.k;
   if (t < p.choice.T) {
-    convert_row<T, kPrepThreads>(reinterpret_cast<const T*>(p.x) + t * p.ldx, p.K, p.xq + (int64_t)t * row_bytes(p.K),
+    convert_row<T, THREADS>(reinterpret_cast<const T*>(p.x) + t * p.ldx, p.K, p.xq + (int64_t)t * row_bytes(p.K),
                                  threadIdx.x);
     return;
   }
-  build_lists<kPrepThreads>(p.choice, lists_at(block, slots), tmp, cap);
-  for (int i = threadIdx.x; i < lists_bytes(slots) / 16; i += kPrepThreads)
+  build_lists<THREADS>(p.choice, lists_at(block, slots), tmp, cap);
+  for (int i = threadIdx.x; i < lists_bytes(slots) / 16; i += THREADS)
     reinterpret_cast<uint4*>(p.lists)[i] = reinterpret_cast<const uint4*>(block)[i];
 }
 
