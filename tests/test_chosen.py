@@ -432,6 +432,24 @@ def test_moe_tokens_do_not_depend_on_their_neighbours(on_gpu):
 
 
 @gpu
+@pytest.mark.parametrize("T", [1, 2, 5, 40])
+@pytest.mark.parametrize("K,I,G", [(192, 320, 64), (384, 128, 128), (256, 768, 256)])
+def test_moe_experts_that_no_token_names_do_not_show(on_gpu, T, K, I, G):
+    E = 5
+    gu, dn = experts(E, K, I, G, BF, 21)
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn((T, K), generator=g).to(BF)
+    ids = torch.tensor([[1, 3]] * T, dtype=torch.int32)
+    w = torch.rand((T, 2), generator=g) + 0.1
+    ref = moe_ref(x, ids, w, gu, dn, G)
+    for i in (0, 2, 4):
+        for t in (gu[1], gu[2], dn[1], dn[2]):
+            t[i] = float("nan")
+    out = on_gpu.moe_experts_awq_w4a16(x.to(DEV), ids.to(DEV), w.to(DEV), *to_dev(gu), *to_dev(dn), group_size=G)
+    assert_rows_close(out, ref, BF)
+
+
+@gpu
 def test_moe_strided_x_in_place_and_workspace_bounds(on_gpu):
     T, E, k, K, I = 10, 4, 2, 192, 128
     gu, dn = experts(E, K, I, 64, FP, 9)
@@ -604,6 +622,22 @@ def test_lora_rows_that_are_not_finite_stay_alone_and_large_v(on_gpu):
 
 
 @gpu
+@pytest.mark.parametrize("M", [2, 60, 400, 700])
+@pytest.mark.parametrize("R", [8, 24, 72, 128])
+def test_lora_adapters_that_no_token_names_do_not_show(on_gpu, M, R):
+    # slots without an adapter may hold anything, NaN too
+    K, N, L = 200, 136, 5
+    x, y, a, b, _, scales = adapters(M, K, N, R, L, BF, BF, 12)
+    ids = torch.where(torch.arange(M) % 3 == 0, 1, 3).to(torch.int32)
+    ids[M // 2] = -1
+    ref = lora_ref(x, y, a, b, ids, scales)
+    for i in (0, 2, 4):
+        a[i], b[i], scales[i] = float("nan"), float("inf"), float("nan")
+    out = on_gpu.lora_add(*[t.to(DEV) for t in (y, x, a, b, ids, scales)])
+    assert_rows_close(out, ref, BF, extra=2.0 ** -15)
+
+
+@gpu
 @pytest.mark.parametrize("M", [64, 1500])
 def test_lora_token_does_not_depend_on_its_tile(on_gpu, M):
     # the same tokens in another order and with other neighbours: the same bits
@@ -678,3 +712,61 @@ def test_one_expert_agrees_with_the_awq_gemv(on_gpu):
     ref = on_gpu.gemv_awq_w4a16(h, *(t[0].to(DEV) for t in dn))
     # gate, up and h are rounded to bf16 there (a few 2^-8 of each, averaged over I), the output in both
     assert_rows_close(out, f64(ref), BF, extra=4 * u_of(BF))
+
+
+@gpu
+def test_weights_beyond_32_bit_offsets(on_gpu):
+    # the last of so many experts and adapters that their bytes and elements pass 2^32; the others are zeros
+    E, K, I, G = 512, 4096, 4096, 256
+    gu, dn = experts(1, K, I, G, BF, 31)
+
+    def last(part, n):
+        out = torch.zeros((n, *part.shape[1:]), device=DEV, dtype=part.dtype)
+        out[-1] = part[0].to(DEV)
+        return out
+
+    for T in (1, 3):
+        x = torch.randn((T, K), generator=torch.Generator().manual_seed(T)).to(BF)
+        ids, w = torch.full((T, 1), E - 1, dtype=torch.int32), torch.ones((T, 1))
+        many = [last(t, E) for t in gu + dn]
+        out = on_gpu.moe_experts_awq_w4a16(x.to(DEV), ids.to(DEV), w.to(DEV), *many, group_size=G)
+        assert_rows_close(out, moe_ref(x, torch.zeros_like(ids), w, gu, dn, G), BF)
+    del many
+    L, K, N, R = 700, 64, 32768, 128
+    for M in (3, 600):
+        x, y, a, b, _, _ = adapters(M, K, N, R, 1, BF, BF, M)
+        ids = torch.full((M,), L - 1, dtype=torch.int32)
+        out = on_gpu.lora_add(y.to(DEV), x.to(DEV), last(a, L), last(b, L), ids.to(DEV))
+        assert_rows_close(out, lora_ref(x, y, a, b, torch.zeros_like(ids), None), BF, extra=2.0 ** -15)
+
+
+@gpu
+def test_calls_from_several_threads_and_streams_at_once(on_gpu):
+    import threading
+    E, k, K, I, R, L = 8, 2, 256, 128, 16, 3
+    gu, dn = experts(E, K, I, 64, BF, 3)
+    gu, dn = to_dev(gu), to_dev(dn)
+    inputs, refs = [], []
+    for i, M in enumerate((1, 5, 33, 64)):
+        x, y, a, b, ids, scales = [t.to(DEV) for t in adapters(M, K, K, R, L, BF, BF, i)]
+        logits = torch.randn((M, E), device=DEV)
+        inputs.append((x, y, a, b, ids, scales, logits))
+        refs.append((on_gpu.lora_add(y, x, a, b, ids, scales), on_gpu.moe_awq_w4a16(x, logits, k, *gu, *dn)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        x, y, a, b, ids, scales, logits = inputs[i]
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [(on_gpu.lora_add(y, x, a, b, ids, scales), on_gpu.moe_awq_w4a16(x, logits, k, *gu, *dn))
+                   for _ in range(40)]
+        stream.synchronize()
+        wrong.extend(i for u, v in got if not (torch.equal(u, refs[i][0]) and torch.equal(v, refs[i][1])))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
