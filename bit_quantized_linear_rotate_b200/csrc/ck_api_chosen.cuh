@@ -163,9 +163,9 @@ cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cud
   return launch_cluster(kern, (unsigned)(tiles * cs), (unsigned)cs, C::kThreads, smem, st, maps, p, stages);
 }
 
-// Workspace: x as fixed point, h as fixed point, the lists.
+// Workspace: rows of x, rows of h, the lists.
 struct MoeWorkspace {
-  size_t xq, hq, lists, total;
+  size_t xr, hr, lists, total;
   MoeWorkspace(int64_t T, int k, int64_t K, int64_t I) {
     size_t at = 0;
     auto take = [&at](int64_t bytes) {
@@ -173,15 +173,15 @@ struct MoeWorkspace {
       at = (at + (size_t)bytes + 255) / 256 * 256;
       return a;
     };
-    xq = take(T * ck::moe::row_bytes((int)K));
-    hq = take(T * k * ck::moe::row_bytes((int)I));
+    xr = take(T * ck::moe::x_row_bytes((int)K));
+    hr = take(T * k * ck::moe::h_row_bytes((int)I));
     lists = take(ck::moe::lists_bytes((int)(T * k)));
     total = at;
   }
 };
 
 // Which kernels a call runs. One or two tokens whose items (64 columns of h of an expert) each get
-// an SM of their own: 16 consumer warps, one CTA an SM, which routes and converts x itself (K = 2048,
+// an SM of their own: 16 consumer warps, one CTA an SM, which routes and orders x itself (K = 2048,
 // top-8 of 64, I = 1024: 14.2 us for one token, 16.0 with prepare_kernel). With a second
 // round of items it loses: the same at two tokens 23.6 against 22.1 us, and K = 4096, I = 4096,
 // top-4 at one 31.8 against 28.4; three and four tokens lose up to 9 us and win 1 at K = 1024.
@@ -191,7 +191,7 @@ struct MoeWorkspace {
 bool moe_self(const ck::moe::Params& p) {
   const int64_t items = (int64_t)p.choice.T * p.choice.k * (p.I / ck::moe::kColsItem);
   return p.choice.T <= ck::moe::kFewTokens && items <= sm_count() &&
-         p.choice.T * p.choice.k <= ck::moe::kFewSlots && p.choice.T * ck::moe::row_bytes(p.K) <= ck::moe::kSelfBytes;
+         p.choice.T * p.choice.k <= ck::moe::kFewSlots && p.choice.T * ck::moe::x_row_bytes(p.K) <= ck::moe::kSelfBytes;
 }
 int moe_token_tiles(const ck::moe::Params& p) {
   const double mean = (double)p.choice.T * p.choice.k / p.choice.E;
@@ -283,8 +283,8 @@ ck_status moe_impl(const char* who, const MoeArgs& a, const ck::moe::Choice& cho
   p.x = a.x; p.ldx = a.ldx; p.K = (int)a.K; p.I = (int)a.I;
   p.gsh = a.G == 64 ? 0 : a.G == 128 ? 1 : 2;
   uint8_t* ws = reinterpret_cast<uint8_t*>(a.ws);
-  p.xq = ws + w.xq;
-  p.hq = ws + w.hq;
+  p.xr = ws + w.xr;
+  p.hr = ws + w.hr;
   p.out = a.out;
   Maps gate_up, down;
   ck_status r = make_expert_maps(&gate_up, a.gq, a.gs, a.gz, a.E, 2 * a.I, a.K, a.G, gate_up_stage_cols(p));

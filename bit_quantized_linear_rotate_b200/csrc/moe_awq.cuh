@@ -5,30 +5,31 @@
 //   out_t   = sum over t's experts of w[t, e] (h[t, e] Wd_e^T)
 //
 // gate_up_kernel computes h, down_kernel the weighted sum. For one or two tokens both choose
-// the experts (or take the choice) in every CTA and gate_up converts x; otherwise
+// the experts (or take the choice) in every CTA and gate_up orders x; otherwise
 // prepare_kernel does that once for all. Each weight that some token
 // needs is read from HBM once (again for each 16 tokens, or fewer, that share an expert), and that
 // bounds the layer: a tile of 16 weight rows x 64 columns (512 packed bytes) takes one of
 // an SM's four schedulers 89 clocks at the measured copy bandwidth, so a tile must cost well
 // under 89 issue slots. Measured, device time and the bytes' time at the copy bandwidth: 16 tokens, top-8
-// of 64 experts, K = 2048, I = 1024 45.9 us (31.0); 32 tokens, top-2 of 8, K = 3840, I = 10240
-// 138 (77.8), there bound by the latency of the consumers' steps (without the products
-// the same loads take 100); one token 14.2 (4.4), bound by three dependent phases: the choice, then
-// the weights of gate and up, then those of down.
+// of 64 experts, K = 2048, I = 1024 70 us (31.0); 32 tokens, top-2 of 8, K = 3840, I = 10240
+// 221 (77.8); one token 18.0 (4.4).
 //
-// Products. Activations enter as 15-bit block fixed point: the 64 columns of a
-// sub-block (which lies in one quantization group, G % 64 == 0) share a scale
-// d = max |x| / 16256, and x ~ d q with q = 128 hi + lo, hi and lo in int8. Then
-//   sum of W x over the sub-block = s (d (128 sum u hi + sum u lo) - 8 X) + z X,  X = d sum q.
-// The sums are exact int32 products of mma.sync.m16n8k32 (16 weight rows, unsigned
-// nibbles; 8 columns of B: hi and lo of four tokens), below 2^24 and so exact as
-// floats, and the rest is 32-bit floating point. The rounding to 15 bits moves x
-// by at most 2^-15 of its block's largest entry, 2^-16 on average against the
-// 2^-9 (bf16) or 2^-12 (fp16) that rounding the result once costs. Nibbles as
-// bf16 numbers in m16n8k16 took 136 instructions a tile, this 50: a packed word is three
-// logical ops, a tile two MMAs, X needs no product.
+// Products. The nibbles become exact 16-bit numbers u - 8 in registers, the A operands of
+// mma.sync.m16n8k16 (16 weight rows); the tokens are the columns of B. For a sub-block of 64
+// columns, which lies in one quantization group (G % 64 == 0),
+//   sum of W x = s P + z X,   P = sum of (u - 8) x,   X = sum of x,
+// with P and X in 32 bits. A weight of zero adds an exact zero to P, however large its x is.
+// * x enters as it is: eight tokens are the columns of B.
+// * h, computed in 32 bits, enters as hi + lo, two fp16 numbers (four tokens' hi and lo are the columns
+//   of B), for both types of x: u - 8 is exact in fp16 too. A power of two for each sub-block
+//   brings its largest magnitude to [2^13, 2^14), so that h may be of any size. hi + lo has
+//   22 bits and two signs: h moves by at most 2^-23 of itself, or where that is more by 2^-25, half of fp16's
+//   smallest step, which is 2^-38 of the sub-block's largest h. Two bf16 numbers would lose 2^-18.
+// (Activations as 15-bit fixed point with a scale for each 64 columns, int8 MMAs, took 46, 138 and 14.8 us for
+// the three cases above, but an entry far above the others of its block cost those their bits:
+// one of 1000 times their size moved them by 3 % of themselves.)
 //
-// A block with an entry that is not finite gets d = NaN: the token's output is NaN.
+// A token with an entry of x that is not finite gets h and outputs that are not.
 //
 // Sums run in a fixed order: the output does not depend on timing.
 #pragma once
@@ -48,21 +49,23 @@ constexpr int kColsItem = 64;          // columns of h in one item of gate_up_ke
 constexpr int kRowsTile = 64;          // output columns of one cluster of down_kernel
 constexpr int kMaxStages = 6;
 
-// Rows of activations as fixed point, in records of four sub-blocks: for each of
-// them 128 bytes, the hi bytes of its 64 columns, then the lo bytes, both in four
-// runs of 16 columns in the order 0 2 4 6 1 3 5 7 8 10 12 14 9 11 13 15 (low nibbles of a packed
-// word, then its high nibbles); behind the four, {d, d, X, X} of each (operands of packed instructions).
-constexpr int kRecord = 4 * 128 + 4 * 16;
-constexpr int kRowPad = 16;            // between tokens in shared memory: four tokens' scales in different banks
-__host__ __device__ constexpr int row_bytes(int columns) { return (columns + 255) / 256 * kRecord; }
+// Rows of activations, in records. Eight columns (a packed word's nibbles) are a piece of 16 bytes in the
+// order 0 4 1 5 2 6 3 7, in which decode() gives that word's nibbles.
+// x: a record is four sub-blocks, each 128 bytes in the order of the pieces; behind them X of each.
+// h: a record is two sub-blocks, each 256 bytes: the even pieces (columns 0-7, 16-23, ...) of hi, those of
+//    lo, the odd ones of hi, those of lo; behind them {d, d, X, X} of each (operands of packed instructions).
+constexpr int kRecord = 512 + 64;
+constexpr int kRowPad = 16;            // between tokens in shared memory: what lanes read at once is in different banks
+__host__ __device__ constexpr int x_row_bytes(int columns) { return (columns + 255) / 256 * kRecord; }
+__host__ __device__ constexpr int h_row_bytes(int columns) { return (columns + 127) / 128 * kRecord; }
 
 struct Params {
   Choice choice;
   const void* x;                       // (T, K) T, row stride ldx
   int64_t ldx;
   int K, I, gsh;                       // quantization group of sub-block sb: sb >> gsh
-  uint8_t* xq;                         // (T) rows of x by prepare_kernel; unused where a CTA converts x itself
-  uint8_t* hq;                         // (slots) rows of h
+  uint8_t* xr;                         // (T) rows of x by prepare_kernel; unused where a CTA orders x itself
+  uint8_t* hr;                         // (slots) rows of h
   uint8_t* lists;                      // by prepare_kernel (lists_at)
   void* out;                           // (T, K) T
 };
@@ -72,32 +75,24 @@ struct Maps {
   CUtensorMap w, s, z;
 };
 
-// ------------------------------------------------------- block fixed point
-
-constexpr float kQMax = 16256.0f;      // 128 * 127
-
-// {scale d, 1 / d} of a block whose largest magnitude is m. Below 2^-100 it counts as zero (1 / d
-// must stay finite); not finite: NaN.
-__device__ __forceinline__ float2 block_scale(float m) {
-  if (!(m < INFINITY)) return make_float2(__int_as_float(0x7fffffff), 0.0f);
-  if (m < 7.9e-31f) return make_float2(0.0f, 0.0f);
-  return make_float2(m * (1.0f / kQMax), kQMax / m);
-}
+// ------------------------------------------------------- rows of activations
 
 // |v| for a maximum that a NaN must not get lost in: as unsigned bits, where NaN is above infinity.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// hi and lo bytes of v / d.
-__device__ __forceinline__ int fixed_point(float v, float inv) {
-  return inv == 0.0f ? 0 : __float2int_rn(v * inv);
+// The power of two that brings a block's largest magnitude (its bits) to [2^13, 2^14), as far as it is a
+// normal number, and its inverse, which scales the block's products. Not finite: {0, NaN}.
+__device__ __forceinline__ float2 block_scale(uint32_t top) {
+  const int e = (int)(top >> 23);
+  if (e == 255) return make_float2(0.0f, __int_as_float(0x7fffffff));
+  const int up = min(126, 140 - e);                  // 13 - (e - 127)
+  return make_float2(__int_as_float((127 + up) << 23), __int_as_float((127 - up) << 23));
 }
 
-__device__ __forceinline__ float4 pair_scales(float d, float x) { return make_float4(d, d, x, x); }
-
-// Converts row `row` of x (K values) by a group of THREADS threads (a multiple of 8), 8 columns
+// Orders row `row` of x (K values) by a group of THREADS threads (a multiple of 8), a piece
 // a thread at a time; lane groups of eight hold a sub-block.
 template <typename T, int THREADS>
-__device__ __forceinline__ void convert_row(const T* x, int K, uint8_t* row, int tid) {
+__device__ __forceinline__ void order_row(const T* x, int K, uint8_t* row, int tid) {
   const int blocks = K >> 6;
   for (int b0 = 0; b0 < blocks; b0 += THREADS / 8) {   // the whole warp stays for the shuffles
     const int sb = b0 + tid / 8, part = tid & 7;
@@ -105,38 +100,24 @@ __device__ __forceinline__ void convert_row(const T* x, int K, uint8_t* row, int
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (in) raw = *reinterpret_cast<const uint4*>(x + sb * 64 + part * 8);
     const T* v = reinterpret_cast<const T*>(&raw);
-    uint32_t m = 0;
+    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, magnitude(awq::Traits<T>::tof(v[i])));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float2 d = block_scale(__uint_as_float(m));
-    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};            // even columns, odd columns
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int f = fixed_point(awq::Traits<T>::tof(v[i]), d.y);
-      const int h = (f + 64) >> 7, l = f - 128 * h;
-      sum += f;
-      hi[i & 1] |= (uint32_t)(h & 0xff) << (8 * (i >> 1));
-      lo[i & 1] |= (uint32_t)(l & 0xff) << (8 * (i >> 1));
-    }
+    for (int i = 0; i < 8; ++i) sum += awq::Traits<T>::tof(v[i]);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (in) {
       uint8_t* rec = row + (sb >> 2) * kRecord;
-      uint8_t* q = rec + (sb & 3) * 128 + part * 8;
-      *reinterpret_cast<uint2*>(q) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(q + 64) = make_uint2(lo[0], lo[1]);
-      if (part == 0) reinterpret_cast<float4*>(rec + 512)[sb & 3] = pair_scales(d.x, d.x * (float)sum);
+      *reinterpret_cast<uint4*>(rec + (sb & 3) * 128 + part * 16) =
+          make_uint4(__byte_perm(raw.x, raw.z, 0x5410), __byte_perm(raw.x, raw.z, 0x7632),
+                     __byte_perm(raw.y, raw.w, 0x5410), __byte_perm(raw.y, raw.w, 0x7632));
+      if (part == 0) reinterpret_cast<float*>(rec + 512)[sb & 3] = sum;
     }
   }
 }
 
 // ----------------------------------------------------------- prepare
 
-
-// CTA t < T: token t's row of x as fixed point. CTA T: the choice and its lists.
+// CTA t < T: token t's row of x in the products' order. CTA T: the choice and its lists.
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS) prepare_kernel(const Params p, int cap) {
   __shared__ ListsTemp tmp;
@@ -145,8 +126,8 @@ __global__ void __launch_bounds__(THREADS) prepare_kernel(const Params p, int ca
   grid_dep_launch();
   const int t = blockIdx.x, slots = p.choice.T * p.choice.k;
   if (t < p.choice.T) {
-    convert_row<T, THREADS>(reinterpret_cast<const T*>(p.x) + t * p.ldx, p.K, p.xq + (int64_t)t * row_bytes(p.K),
-                                 threadIdx.x);
+    order_row<T, THREADS>(reinterpret_cast<const T*>(p.x) + t * p.ldx, p.K, p.xr + (int64_t)t * x_row_bytes(p.K),
+                          threadIdx.x);
     return;
   }
   build_lists<THREADS>(p.choice, lists_at(block, slots), tmp, cap);
@@ -172,36 +153,51 @@ __device__ __forceinline__ int tile_offset(int r, int sb, int t) {
   return r * 128 + (((2 * sb + (t >> 1)) ^ (r & 7)) << 4) + 8 * (t & 1);
 }
 
-// A tile of 16 weight rows x 64 columns as the A operands of two MMAs: the lane's bytes of rows r and r + 1.
-__device__ __forceinline__ void load_tile(const uint8_t* row0, const uint8_t* row1, uint32_t (&a)[2][4]) {
+// A packed word's nibbles as u - 8, exact, in four pairs of 16-bit numbers: columns (0, 4), (1, 5), (2, 6), (3, 7).
+template <typename T>
+__device__ __forceinline__ void decode(uint32_t w, uint32_t (&p)[4]) {
+  if constexpr (std::is_same<T, __half>::value) {
+    // 0x6400 | u is 1024 + u, 0x6400 | 16 u is 1024 + 16 u: one shift a word in place of three
+    const __half2 bias = __float2half2_rn(-1032.0f), part = __float2half2_rn(0.0625f), rest = __float2half2_rn(-72.0f);
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t v = w >> (4 * i), a = (v & 0x000F000Fu) | 0x64006400u, b = (v & 0x00F000F0u) | 0x64006400u;
+      const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), bias);
+      const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&b), part, rest);
+      p[i] = *reinterpret_cast<const uint32_t*>(&x);
+      p[i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = awq::nib_pair<T>(w, i);
+  }
+}
+
+// A tile of 16 weight rows x 64 columns as the A operands of four MMAs: the lane's 16 columns of rows r and r + 1.
+template <typename T>
+__device__ __forceinline__ void load_tile(const uint8_t* row0, const uint8_t* row1, uint32_t (&a)[4][4]) {
   const uint2 w0 = *reinterpret_cast<const uint2*>(row0), w1 = *reinterpret_cast<const uint2*>(row1);
-  a[0][0] = w0.x & 0x0F0F0F0Fu;
-  a[0][1] = w1.x & 0x0F0F0F0Fu;
-  a[0][2] = (w0.x >> 4) & 0x0F0F0F0Fu;
-  a[0][3] = (w1.x >> 4) & 0x0F0F0F0Fu;
-  a[1][0] = w0.y & 0x0F0F0F0Fu;
-  a[1][1] = w1.y & 0x0F0F0F0Fu;
-  a[1][2] = (w0.y >> 4) & 0x0F0F0F0Fu;
-  a[1][3] = (w1.y >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t p[4], q[4];
+    decode<T>(i == 0 ? w0.x : w0.y, p);
+    decode<T>(i == 0 ? w1.x : w1.y, q);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      a[2 * i + j][0] = p[2 * j], a[2 * i + j][1] = q[2 * j];
+      a[2 * i + j][2] = p[2 * j + 1], a[2 * i + j][3] = q[2 * j + 1];
+    }
+  }
 }
 
-__device__ __forceinline__ void mma_u8s8(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// tot += the sub-block's sum of W x = s (d I - 8 X) + z X, for the tile's rows r and r + 1 (packed: three
-// instructions for six) and token t of the four in b. dx: that token's {d, d, X, X}, x8: {-8 X, -8 X}.
-__device__ __forceinline__ void add_block(float2& tot, const uint32_t (&a)[2][4], const uint4 b, const float2 s,
-                                          const float2 z, const float4 dx, const float2 x8) {
-  int c[4] = {0, 0, 0, 0};
-  mma_u8s8(c, a[0], b.x, b.y);
-  mma_u8s8(c, a[1], b.z, b.w);
-  const float2 i2 = make_float2((float)(c[0] * 128 + c[1]), (float)(c[2] * 128 + c[3]));
-  tot = __ffma2_rn(s, __ffma2_rn(make_float2(dx.x, dx.y), i2, x8), tot);
-  tot = __ffma2_rn(z, make_float2(dx.z, dx.w), tot);
+// c = the sub-block's sums of (u - 8) times the columns of B, whose 16 columns of this lane are the pieces b0, b1.
+template <typename T>
+__device__ __forceinline__ void multiply(float (&c)[4], const uint32_t (&a)[4][4], const uint4 b0, const uint4 b1) {
+  c[0] = c[1] = c[2] = c[3] = 0.0f;
+  awq::Traits<T>::mma(c, a[0], b0.x, b0.y);
+  awq::Traits<T>::mma(c, a[1], b0.z, b0.w);
+  awq::Traits<T>::mma(c, a[2], b1.x, b1.y);
+  awq::Traits<T>::mma(c, a[3], b1.z, b1.w);
 }
 
 // ------------------------------------------------------------------ the ring
@@ -300,7 +296,7 @@ struct GateUp {
   static constexpr int kStage = (2 * kW + 4 * kS + kRows + 1023) / 1024 * 1024;
   static constexpr int kRed = KW * 4 * 2 * NT * 32 * 8;         // float2 [kw][rq][gate, up][token tile][lane]
   static_assert(sizeof(FewTemp) <= kRed, "the choice is handed on in it");
-  __host__ __device__ static constexpr int sums(int T, int K) { return kRed + (SELF ? T * row_bytes(K) : 0); }
+  __host__ __device__ static constexpr int sums(int T, int K) { return kRed + (SELF ? T * x_row_bytes(K) : 0); }
 };
 
 template <typename T, int NT, int KW, bool SELF>
@@ -324,15 +320,15 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
   }
   grid_dep_wait();
   grid_dep_launch();   // after the wait: the next kernel may read the choice before its own wait
-  const int xrow = row_bytes(p.K);
-  if constexpr (SELF) {                // warps 0-3 choose while the others convert x
+  const int xrow = x_row_bytes(p.K);
+  if constexpr (SELF) {                // warps 0 and 1 choose (a token each) while the others order x
     FewTemp& few = *reinterpret_cast<FewTemp*>(red);
-    constexpr int kConvert = C::kThreads - 32 * kFewTokens;
+    constexpr int kOrder = C::kThreads - 32 * kFewTokens;
     if (warp < kFewTokens) {
       choose_few(p.choice, few);
     } else {
       for (int i = 0; i < tokens; ++i)
-        convert_row<T, kConvert>(reinterpret_cast<const T*>(p.x) + i * p.ldx, p.K, own + i * xrow, tid - 32 * kFewTokens);
+        order_row<T, kOrder>(reinterpret_cast<const T*>(p.x) + i * p.ldx, p.K, own + i * xrow, tid - 32 * kFewTokens);
     }
     __syncthreads();
     list_few(p.choice, L, few);
@@ -355,7 +351,7 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
       const int u = item / per_unit, c0 = (item % per_unit) * kColsItem;
       const int e = L.unit_expert[u], row = e * 2 * p.I + c0, n = L.unit_n[u];
       const uint8_t* xr = nullptr;
-      if (!SELF && lane < n) xr = p.xq + (int64_t)L.slot_token[L.unit_start[u] + lane] * xrow;
+      if (!SELF && lane < n) xr = p.xr + (int64_t)L.slot_token[L.unit_start[u] + lane] * xrow;
       for (int ch = 0; ch < nchunk; ++ch, at.next(stages)) {
         live = __all_sync(0xffffffffu, ring_claim(R, at));
         if (!live) break;
@@ -390,24 +386,28 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
   const int tile = tile_offset(16 * rq + 2 * g, kw, t);
   const int sc0 = (kw >> p.gsh) * 128 + 32 * rq + 4 * g, sc1 = ((kw + KW) >> p.gsh) * 128 + 32 * rq + 4 * g;
   Cursor at;
-  float2 tot[2][NT];
-  // One item's products with N token tiles; sums in tot.
+  constexpr int N8 = (NT + 1) / 2;       // tiles of eight tokens
+  float2 tot[2][N8][2];                  // gate and up: rows r and r + 1 for tokens 2 t and 2 t + 1 of a tile
+  // One item's products with N tiles; sums in tot.
   auto products = [&](auto tiles, int start, int n) {
     constexpr int N = decltype(tiles)::value;
-    // the lane's column of B (hi or lo of token g / 2) and the scales of token t; past the last
+    // the lane's column of B (token g) and where the X of tokens 2 t and 2 t + 1 are; past the last
     // token its copies, whose results nobody reads
-    int bq[N], bs[N];
+    int bq[N], bx[N][2];
+    auto row_of = [&](int c) {
+      c = min(c, n - 1);
+      return SELF ? L.slot_token[start + c] * xrow : c * C::kRow;
+    };
 #pragma unroll
     for (int tt = 0; tt < N; ++tt) {
-      const int c = min(4 * tt + (g >> 1), n - 1), d = min(4 * tt + t, n - 1);
-      const int rows = SELF ? xrow : C::kRow;
-      bq[tt] = (SELF ? L.slot_token[start + c] : c) * rows + kw * 128 + (g & 1) * 64 + t * 16;
-      bs[tt] = (SELF ? L.slot_token[start + d] : d) * rows + 512 + kw * 16;
+      bq[tt] = row_of(8 * tt + g) + kw * 128 + t * 32;
+      bx[tt][0] = row_of(8 * tt + 2 * t) + 512 + kw * 4;
+      bx[tt][1] = row_of(8 * tt + 2 * t + 1) + 512 + kw * 4;
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int tt = 0; tt < N; ++tt) tot[m][tt] = make_float2(0.0f, 0.0f);
+      for (int tt = 0; tt < N; ++tt) tot[m][tt][0] = tot[m][tt][1] = make_float2(0.0f, 0.0f);
     for (int ch = 0; ch < nchunk; ++ch, at.next(stages)) {
       const uint8_t* st = ring + at.stage * C::kStage;
       const uint8_t* rec = SELF ? own + ch * (C::kSubs / 4) * kRecord : st + 2 * C::kW + 4 * C::kS;
@@ -420,22 +420,31 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
         const uint8_t* row0 = st + (KW == 2 && i == 1 ? tile ^ 64 : tile) + (KW == 4 ? i * 64 * 128 : 0);
         const uint8_t* row1 = st + 128 + (KW == 2 && i == 1 ? tile ^ 80 : tile ^ 16) + (KW == 4 ? i * 64 * 128 : 0);
         const uint8_t* sp = st + 2 * C::kW + (i == 0 ? sc0 : sc1);
-        uint4 b[N];
-        float4 dx[N];
-        float2 x8[N];
+        uint4 b[N][2];
+        float2 X[N];
 #pragma unroll
         for (int tt = 0; tt < N; ++tt) {
-          b[tt] = *reinterpret_cast<const uint4*>(rec + bq[tt] + (KW == 4 ? i * kRecord : i * 256));
-          dx[tt] = *reinterpret_cast<const float4*>(rec + bs[tt] + (KW == 4 ? i * kRecord : i * 32));
-          x8[tt] = __fmul2_rn(make_float2(-8.0f, -8.0f), make_float2(dx[tt].z, dx[tt].w));
+          const uint8_t* bp = rec + bq[tt] + (KW == 4 ? i * kRecord : i * 256);
+          b[tt][0] = *reinterpret_cast<const uint4*>(bp);
+          b[tt][1] = *reinterpret_cast<const uint4*>(bp + 16);
+          const int at_x = KW == 4 ? i * kRecord : i * 8;
+          X[tt] = make_float2(*reinterpret_cast<const float*>(rec + bx[tt][0] + at_x),
+                              *reinterpret_cast<const float*>(rec + bx[tt][1] + at_x));
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {    // gate, up
-          uint32_t a[2][4];
-          load_tile(row0 + m * C::kW, row1 + m * C::kW, a);
+          uint32_t a[4][4];
+          load_tile<T>(row0 + m * C::kW, row1 + m * C::kW, a);
           const float2 s = load_pair<T>(sp + 2 * m * C::kS), z = load_pair<T>(sp + 2 * m * C::kS + C::kS);
 #pragma unroll
-          for (int tt = 0; tt < N; ++tt) add_block(tot[m][tt], a, b[tt], s, z, dx[tt], x8[tt]);
+          for (int tt = 0; tt < N; ++tt) {
+            float c[4];
+            multiply<T>(c, a, b[tt][0], b[tt][1]);
+            tot[m][tt][0] = __ffma2_rn(make_float2(s.x, s.x), make_float2(c[0], c[1]), tot[m][tt][0]);
+            tot[m][tt][1] = __ffma2_rn(make_float2(s.y, s.y), make_float2(c[2], c[3]), tot[m][tt][1]);
+            tot[m][tt][0] = __ffma2_rn(make_float2(z.x, z.x), X[tt], tot[m][tt][0]);
+            tot[m][tt][1] = __ffma2_rn(make_float2(z.y, z.y), X[tt], tot[m][tt][1]);
+          }
         }
       }
       ring_release(R, at);
@@ -445,16 +454,20 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
   for (int item = blockIdx.x, turn = 0; item < items; item += gridDim.x, ++turn) {
     const int u = item / per_unit, cb = item % per_unit;
     const int start = L.unit_start[u], n = L.unit_n[u], nt = (n + 3) >> 2;
-    if (NT == 1 || n <= 4) products(std::integral_constant<int, 1>(), start, n);
-    else if (NT == 2 || n <= 8) products(std::integral_constant<int, NT < 2 ? 1 : 2>(), start, n);
-    else if (n <= 12) products(std::integral_constant<int, NT < 3 ? 1 : 3>(), start, n);
-    else products(std::integral_constant<int, NT>(), start, n);
+    if (N8 == 1 || n <= 8) products(std::integral_constant<int, 1>(), start, n);
+    else products(std::integral_constant<int, N8>(), start, n);
     if (turn != 0) consumers_sync<32 * C::kCons>();   // the previous item's sums have been read
+    // in red's tiles of four tokens lane 4 g' + t' holds rows 2 g' and 2 g' + 1 for token t'
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int tt = 0; tt < NT; ++tt)
-        if (tt < nt) red[((warp * 2 + m) * NT + tt) * 32 + lane] = tot[m][tt];
+      for (int tt = 0; tt < N8; ++tt) {
+        const int four = 2 * tt + (t >> 1);
+        const float2 u = tot[m][tt][0], v = tot[m][tt][1];
+        if (four < nt)
+          *reinterpret_cast<float4*>(&red[((warp * 2 + m) * NT + four) * 32 + 4 * g + 2 * (t & 1)]) =
+              make_float4(u.x, v.x, u.y, v.y);
+      }
     consumers_sync<32 * C::kCons>();
     // Token c of the unit: a lane forms columns 2 lane and 2 lane + 1. The other warps go on.
     for (int c = (warp + turn) & (C::kCons - 1); c < n; c += C::kCons) {
@@ -466,23 +479,26 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
         const float2 a = q[0], b = q[NT * 32];
         gate.x += a.x, gate.y += a.y, up.x += b.x, up.y += b.y;
       }
-      const float h0 = gate.x / (1.0f + expf(-gate.x)) * up.x, h1 = gate.y / (1.0f + expf(-gate.y)) * up.y;
-      const uint32_t most = __reduce_max_sync(0xffffffffu, max(magnitude(h0), magnitude(h1)));
-      const float2 d = block_scale(__uint_as_float(most));
-      const int f0 = fixed_point(h0, d.y), f1 = fixed_point(h1, d.y);
-      const int a0 = (f0 + 64) >> 7, a1 = (f1 + 64) >> 7;
-      const int sum = __reduce_add_sync(0xffffffffu, f0 + f1);
-      // columns 8 i + 2 j and + 1 (i = lane / 4, j = lane % 4): byte j of the run's even and odd words
-      uint8_t* rec = p.hq + (int64_t)(start + c) * row_bytes(p.I) + (cb >> 2) * kRecord;
-      uint8_t* q = rec + (cb & 3) * 128 + (lane >> 2) * 8 + (lane & 3);
-      q[0] = (uint8_t)a0;
-      q[4] = (uint8_t)a1;
-      q[64] = (uint8_t)(f0 - 128 * a0);
-      q[68] = (uint8_t)(f1 - 128 * a1);
-      if (lane == 0) {                   // with the token's weight: down_kernel only adds
-        const float w = L.slot_w[start + c];
-        reinterpret_cast<float4*>(rec + 512)[cb & 3] = pair_scales(w * d.x, w * (d.x * (float)sum));
-      }
+      // with the token's weight: down_kernel only adds
+      const float w = L.slot_w[start + c];
+      const float h0 = w * (gate.x / (1.0f + expf(-gate.x)) * up.x), h1 = w * (gate.y / (1.0f + expf(-gate.y)) * up.y);
+      const float2 d = block_scale(__reduce_max_sync(0xffffffffu, max(magnitude(h0), magnitude(h1))));
+      float sum = h0 + h1;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      // hi and lo of h d.x; zeros where the block is not finite (its products get d.y = NaN)
+      const float v0 = d.x == 0.0f ? 0.0f : h0 * d.x, v1 = d.x == 0.0f ? 0.0f : h1 * d.x;
+      const __half hi0 = __float2half_rn(v0), hi1 = __float2half_rn(v1);
+      const __half lo0 = __float2half_rn(v0 - __half2float(hi0)), lo1 = __float2half_rn(v1 - __half2float(hi1));
+      // columns 8 i + 2 j and + 1 (i = lane / 4, j = lane % 4): of piece i, places 0 2, 4 6, 1 3, 5 7 by j
+      uint8_t* rec = p.hr + (int64_t)(start + c) * h_row_bytes(p.I) + (cb >> 1) * kRecord;
+      __half* q = reinterpret_cast<__half*>(rec + (cb & 1) * 256 + ((lane >> 2) & 1) * 128 + (lane >> 3) * 16) +
+                  4 * (lane & 1) + ((lane >> 1) & 1);
+      q[0] = hi0;
+      q[2] = hi1;
+      q[32] = lo0;
+      q[34] = lo1;
+      if (lane == 0) reinterpret_cast<float4*>(rec + 512)[cb & 1] = make_float4(d.y, d.y, sum, sum);
     }
   }
 }
@@ -516,7 +532,8 @@ struct Down {
   static constexpr int kSubs = 4 * SUB;
   static constexpr int kW = kSubs * 64 * 32;
   static constexpr int kS = kSubs * 128;
-  static constexpr int kRow = SUB * kRecord + kRowPad;
+  static constexpr int kRecs = kSubs / 2;        // records of h a step
+  static constexpr int kRow = kRecs * kRecord + kRowPad;
   static constexpr int kStage = (kW + 2 * kS + 4 * NT * kRow + 1023) / 1024 * 1024;
   __host__ __device__ static constexpr int sums(int T) { return 4 * T * kRowsTile * 4; }
 };
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(Down<NT>::kThreads, 2)
 
   const int nsub = p.I >> 6, nchunk = (nsub + C::kSubs - 1) / C::kSubs;
   const int srows = C::kSubs >> p.gsh;
-  const int hrow = row_bytes(p.I);
+  const int hrow = h_row_bytes(p.I), nrec = (nsub + 1) >> 1;
   // This CTA's steps: with many chunks a unit, every ranks-th chunk of each unit (units of many
   // and of few tokens mix); else a contiguous share.
   const int units = L.units();
@@ -582,17 +599,18 @@ __global__ void __launch_bounds__(Down<NT>::kThreads, 2)
       uint8_t* st = ring + at.stage * C::kStage;
       uint64_t* bar = &R.full[at.stage];
       const int boxes = min(SUB, (nsub - C::kSubs * ch + 3) >> 2);
-      mbar_arrive_expect_tx(bar, boxes * (64 * 128 + L.unit_n[u] * kRecord) + 2 * 128 * srows);
+      const int recs = min(C::kRecs, nrec - C::kRecs * ch);
+      mbar_arrive_expect_tx(bar, boxes * 64 * 128 + L.unit_n[u] * recs * kRecord + 2 * 128 * srows);
       for (int i = 0; i < boxes; ++i)
         tma_load_2d(st + i * 64 * 128, &maps.w, bar, (C::kSubs * ch + 4 * i) * 32, e * p.K + n0);
       tma_load_2d(st + C::kW, &maps.s, bar, n0, e * ngrp + ch * srows);
       tma_load_2d(st + C::kW + C::kS, &maps.z, bar, n0, e * ngrp + ch * srows);
     };
     auto fetch_rows = [&](int u, int ch, const Cursor& at) {
-      const int boxes = min(SUB, (nsub - C::kSubs * ch + 3) >> 2);
+      const int recs = min(C::kRecs, nrec - C::kRecs * ch);
       if (lane < L.unit_n[u])
         bulk_load(ring + at.stage * C::kStage + C::kW + 2 * C::kS + lane * C::kRow,
-                  p.hq + (int64_t)(L.unit_start[u] + lane) * hrow + ch * SUB * kRecord, boxes * kRecord,
+                  p.hr + (int64_t)(L.unit_start[u] + lane) * hrow + ch * C::kRecs * kRecord, recs * kRecord,
                   &R.full[at.stage]);
     };
     const int ahead = min(stages, left);
@@ -636,8 +654,9 @@ __global__ void __launch_bounds__(Down<NT>::kThreads, 2)
       int bq[N], bs[N];
 #pragma unroll
       for (int tt = 0; tt < N; ++tt) {
-        bq[tt] = min(4 * tt + (g >> 1), n - 1) * C::kRow + kw * 128 + (g & 1) * 64 + t * 16;
-        bs[tt] = min(4 * tt + t, n - 1) * C::kRow + 512 + kw * 16;
+        // the lane's column of B is hi or lo of token g / 2; the scales are those of token t
+        bq[tt] = min(4 * tt + (g >> 1), n - 1) * C::kRow + (kw >> 1) * kRecord + (kw & 1) * 256 + (g & 1) * 64 + t * 16;
+        bs[tt] = min(4 * tt + t, n - 1) * C::kRow + (kw >> 1) * kRecord + 512 + (kw & 1) * 16;
       }
       float2 tot[2][N];
 #pragma unroll
@@ -649,25 +668,29 @@ __global__ void __launch_bounds__(Down<NT>::kThreads, 2)
 #pragma unroll
         for (int i = 0; i < SUB; ++i) {
           if (C::kSubs * ch + kw + 4 * i >= nsub) break;
-          uint4 b[N];
-          float4 dx[N];
-          float2 x8[N];
-#pragma unroll
-          for (int tt = 0; tt < N; ++tt) {
-            b[tt] = *reinterpret_cast<const uint4*>(rec + bq[tt] + i * kRecord);
-            dx[tt] = *reinterpret_cast<const float4*>(rec + bs[tt] + i * kRecord);
-            x8[tt] = __fmul2_rn(make_float2(-8.0f, -8.0f), make_float2(dx[tt].z, dx[tt].w));
-          }
           const uint8_t* row0 = st + tile + i * 64 * 128;
           const uint8_t* row1 = st + 128 + (tile ^ 16) + i * 64 * 128;
           const uint8_t* sp = st + C::kW + (i == 0 ? sc0 : sc1);
+          uint32_t a[2][4][4];
+          float2 sc[2], z[2];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            uint32_t a[2][4];
-            load_tile(row0 + m * 16 * 128, row1 + m * 16 * 128, a);
-            const float2 sc = load_pair<T>(sp + 32 * m), z = load_pair<T>(sp + 32 * m + C::kS);
+            load_tile<__half>(row0 + m * 16 * 128, row1 + m * 16 * 128, a[m]);
+            sc[m] = load_pair<T>(sp + 32 * m), z[m] = load_pair<T>(sp + 32 * m + C::kS);
+          }
 #pragma unroll
-            for (int tt = 0; tt < N; ++tt) add_block(tot[m][tt], a, b[tt], sc, z, dx[tt], x8[tt]);
+          for (int tt = 0; tt < N; ++tt) {
+            const uint8_t* bp = rec + bq[tt] + i * 2 * kRecord;
+            const uint4 b0 = *reinterpret_cast<const uint4*>(bp), b1 = *reinterpret_cast<const uint4*>(bp + 128);
+            const float4 dx = *reinterpret_cast<const float4*>(rec + bs[tt] + i * 2 * kRecord);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              float c[4];
+              multiply<__half>(c, a[m], b0, b1);
+              const float2 v = __fmul2_rn(make_float2(dx.x, dx.y), make_float2(c[0] + c[1], c[2] + c[3]));
+              tot[m][tt] = __ffma2_rn(sc[m], v, tot[m][tt]);
+              tot[m][tt] = __ffma2_rn(z[m], make_float2(dx.z, dx.w), tot[m][tt]);
+            }
           }
         }
         ring_release(R, at);

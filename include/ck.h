@@ -403,10 +403,9 @@ ck_status ck_moe_route(const void* logits, ck_dtype lt, int64_t T, int64_t E, in
  *   h       = silu(x Wgate^T) * (x Wup^T)                 (float32 accumulation)
  *   out[t]  = sum over t's experts of weight * (h Wdown^T)
  * rounded once, to dt. The weights are read only of experts that some token goes
- * to, once for each 16 of its tokens or fewer. No h goes through bf16 or fp16.
- * x and h enter the products as 15-bit block fixed point: in each block of 64
- * columns a value moves by at most 2^-15 of the block's largest magnitude, and
- * a block whose largest magnitude is below 2^-100 counts as zero.
+ * to, once for each 16 of its tokens or fewer. x enters the products as it is, h
+ * in 22 bits and more: in each block of 64 columns a value moves by at most 2^-23
+ * of itself or 2^-38 of the block's largest magnitude.
  * dt applies to x, the scales, the zeros and out (bf16 or fp16).
  * x         : (T, K), row stride ldx >= K elements, ldx % 8 == 0; 0 <= T <= 64.
  * gate_up_q : (E, 2 I, K/2) packed uint4, each expert's I gate rows, then its
