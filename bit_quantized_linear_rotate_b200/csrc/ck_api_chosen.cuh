@@ -304,7 +304,7 @@ cudaError_t launch_lora_few(const ck::lora::Params& p, int64_t tiles, cudaStream
   using namespace ck::lora;
   auto kern = lora_kernel<T, TY, RC>;
   struct Tag {};
-  const int smem = (int)sizeof(Smem<RC>);
+  const int smem = (int)sizeof(Smem<RC, VOperand<T>::kPlanes>);
   const cudaError_t e = set_smem_max<Tag>(kern, smem, smem);
   if (e != cudaSuccess) return e;
   // The cluster size by the time expected: rounds of as many clusters as run at once, each a share of a tile's
@@ -327,7 +327,7 @@ cudaError_t launch_lora_few(const ck::lora::Params& p, int64_t tiles, cudaStream
 template <typename T, typename TY, int RB>
 cudaError_t launch_lora_tc(const ck::lora::Params& p, int64_t tiles, cudaStream_t st) {
   using namespace ck::lora;
-  using C = LoraTc<RB>;
+  using C = LoraTc<RB, VOperand<T>::kPlanes>;
   auto kern = lora_tc_kernel<T, TY, RB>;
   struct Tag {};
   const cudaError_t e = set_smem_max<Tag>(kern, C::kSmem, C::kSmem);

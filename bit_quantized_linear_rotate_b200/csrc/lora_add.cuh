@@ -17,9 +17,10 @@
 // neighbouring MMAs are numbered so that a lane's results are eight consecutive
 // n of y: 16-byte loads and stores.
 //
-// v enters the expand as hi + lo of the inputs' 16-bit type, hi = round(v) and
-// lo = round(v - hi): what is lost is at most 2^-17 (bf16) or 2^-22 (fp16) of v. For
-// fp16 each row of v is first scaled by a power of two, which brings its
+// v, a sum in 32 bits, enters the expand as a sum of numbers of the inputs' 16-bit type, each
+// the rounding of what those before it leave (B's type is also the operand's). Three bf16 numbers hold all
+// 24 bits of v (two lose up to 2^-18 of it, which shows where ranks cancel); two fp16 numbers hold
+// it to 2^-23. For fp16 each row of v is first scaled by a power of two, which brings its
 // largest entry to [2^13, 2^14): v itself may lie outside fp16's range.
 //
 // A token's arithmetic does not depend on which tile it is in or which tokens
@@ -309,9 +310,16 @@ __device__ __forceinline__ int find_tile(const Params& p, int tile, int (&token)
 
 static_assert(kSelfGroup + 16 <= kPickBytes / 4, "find_tile's scratch");
 
-template <typename T> struct Half2Of;
-template <> struct Half2Of<__nv_bfloat16> { static constexpr bool kScaled = false; };
-template <> struct Half2Of<__half> { static constexpr bool kScaled = true; };
+// How v enters the expand: as kPlanes numbers of type T, with or without a power of two for each row.
+template <typename T> struct VOperand;
+template <> struct VOperand<__nv_bfloat16> {
+  static constexpr int kPlanes = 3;
+  static constexpr bool kScaled = false;
+};
+template <> struct VOperand<__half> {
+  static constexpr int kPlanes = 2;
+  static constexpr bool kScaled = true;
+};
 
 // The power of two that brings a row's largest magnitude (its bits) to [2^13, 2^14); 0 where it is zero,
 // subnormal or not finite.
@@ -321,12 +329,15 @@ __device__ __forceinline__ int scale_exponent(uint32_t top) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// v as hi + lo; an infinity stays one.
-template <typename T>
-__device__ __forceinline__ void split(float v, T& hi, T& lo) {
-  hi = awq::Traits<T>::fromf(v);
-  const float h = awq::Traits<T>::tof(hi);
-  lo = awq::Traits<T>::fromf(isfinite(h) ? v - h : 0.0f);
+// v as a sum of P numbers, the largest first; an infinity stays one.
+template <typename T, int P>
+__device__ __forceinline__ void split(float v, T (&part)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    part[i] = awq::Traits<T>::fromf(v);
+    const float f = awq::Traits<T>::tof(part[i]);
+    v = isfinite(f) ? v - f : 0.0f;
+  }
 }
 
 // Columns [c0, c1) of y's rows token[0 .. n) into out (nothing where out is y): a row a warp, eight
@@ -357,30 +368,31 @@ __device__ __forceinline__ void copy_rows(const TY* y, TY* out, const Params& p,
   }
 }
 
-// Shared memory of a CTA: RC 32-wide chunks of rank.
+// Shared memory of a CTA: RC 32-wide chunks of rank, v as P numbers.
 constexpr int kFewTile = 16;                          // tokens of a tile
-template <int RC>
+template <int RC, int P>
 struct alignas(16) Smem {
   static constexpr int kR = 32 * RC;
   static constexpr int kVStride = kR + 8;             // 16-bit elements: rows 16 bytes apart in the banks
   float part[kWarps][kFewTile][kR];                         // the warps' sums; [0]: this CTA's
   float v[kFewTile][kR];                                    // the cluster's
-  uint16_t hi[kFewTile][kVStride], lo[kFewTile][kVStride];
+  uint16_t planes[P][kFewTile][kVStride];                   // v as the expand's operand
   float row_scale[kFewTile];
   int token[kFewTile];
   int scratch[kPickBytes / 4];
 };
 
 // Many small CTAs hide each other's latencies (ranks up to 32: three an SM, else two; 64 tokens with adapters of
-// rank 128, K = N = 4096: 27.4 us, 32.5 with one). Latency bounds them: several loads of a step are
+// rank 128, K = N = 4096: 28.8 us; with v as two numbers 27.4, and 32.5 with one CTA). Latency bounds them: several loads of a step are
 // issued before its first product, those of y before those of B (a decode step of 64 tokens, K = 4096,
-// N = 12288, R = 32, 48 adapters 16.7 us, 20.0 with a load for each product; its bytes take 6.3 at
-// the measured copy bandwidth). Bringing B into shared memory from the start took the place
+// N = 12288, R = 32, 48 adapters 18.1 us, 16.5 with v as two bf16 numbers; with those 20.0 with a load for each
+// product; its bytes take 6.3 at the measured copy bandwidth). Bringing B into shared memory from the start took the place
 // of CTAs on the SMs: 29 us for that decode step.
 template <typename T, typename TY, int RC>
 __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t sm[];
-  using SM = Smem<RC>;
+  constexpr int P = VOperand<T>::kPlanes;
+  using SM = Smem<RC, P>;
   using Tr = awq::Traits<T>;
   SM& S = *reinterpret_cast<SM*>(sm);
   constexpr int RT = 4 * RC;
@@ -473,14 +485,14 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
   }
   cluster_sync();
 
-  // ---- v as hi + lo
+  // ---- v as the expand's operand
   const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
   for (int m = warp; m < n; m += kWarps) {
     float v[RC];
     int ex = 0;
 #pragma unroll
     for (int i = 0; i < RC; ++i) v[i] = S.v[m][32 * i + lane];
-    if constexpr (Half2Of<T>::kScaled) {
+    if constexpr (VOperand<T>::kScaled) {
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < RC; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
@@ -489,10 +501,10 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
     const float up = exp2_int(ex);
 #pragma unroll
     for (int i = 0; i < RC; ++i) {
-      T h, l;
-      split(v[i] * up, h, l);
-      S.hi[m][32 * i + lane] = *reinterpret_cast<const uint16_t*>(&h);
-      S.lo[m][32 * i + lane] = *reinterpret_cast<const uint16_t*>(&l);
+      T part[P];
+      split(v[i] * up, part);
+#pragma unroll
+      for (int k = 0; k < P; ++k) S.planes[k][m][32 * i + lane] = *reinterpret_cast<const uint16_t*>(&part[k]);
     }
     if (lane == 0) S.row_scale[m] = as * exp2_int(-ex);
   }
@@ -527,16 +539,16 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
       for (int rc = 0; rc < kBatch; ++rc) {
         if (32 * (r0 + rc) >= p.R) break;
         const int at = 32 * (r0 + rc) + 8 * t;
-        const uint4 h0 = *reinterpret_cast<const uint4*>(&S.hi[g][at]), h1 = *reinterpret_cast<const uint4*>(&S.hi[g + 8][at]);
-        const uint4 l0 = *reinterpret_cast<const uint4*>(&S.lo[g][at]), l1 = *reinterpret_cast<const uint4*>(&S.lo[g + 8][at]);
-        const uint32_t ha[4] = {h0.x, h1.x, h0.y, h1.y}, hb[4] = {h0.z, h1.z, h0.w, h1.w};
-        const uint32_t la[4] = {l0.x, l1.x, l0.y, l1.y}, lb[4] = {l0.z, l1.z, l0.w, l1.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          Tr::mma(c[j], ha, w[rc][j].x, w[rc][j].y);
-          Tr::mma(c[j], hb, w[rc][j].z, w[rc][j].w);
-          Tr::mma(c[j], la, w[rc][j].x, w[rc][j].y);
-          Tr::mma(c[j], lb, w[rc][j].z, w[rc][j].w);
+        for (int k = 0; k < P; ++k) {
+          const uint4 v0 = *reinterpret_cast<const uint4*>(&S.planes[k][g][at]);
+          const uint4 v1 = *reinterpret_cast<const uint4*>(&S.planes[k][g + 8][at]);
+          const uint32_t fa[4] = {v0.x, v1.x, v0.y, v1.y}, fb[4] = {v0.z, v1.z, v0.w, v1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            Tr::mma(c[j], fa, w[rc][j].x, w[rc][j].y);
+            Tr::mma(c[j], fb, w[rc][j].z, w[rc][j].w);
+          }
         }
       }
     }

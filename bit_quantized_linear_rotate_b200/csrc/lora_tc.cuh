@@ -2,7 +2,7 @@
 // the tcgen05 tensor cores.
 //
 //   shrink: v (128 x R)  = x A^T      M = 128 tokens, N = R, K in blocks of 64
-//   expand: d (128 x N)  = v B^T      M = 128 tokens, N in blocks of 128, K = R, as hi + lo
+//   expand: d (128 x N)  = v B^T      M = 128 tokens, N in blocks of 128, K = R for each number that v is split into
 //   out = y + scale d
 //
 // A cluster of CTAs owns a tile: each CTA takes a share of K for the shrink,
@@ -12,7 +12,7 @@
 // R = 64; tiles of 64 tokens read it twice as often). The tensor cores
 // read their operands from shared memory themselves, which leaves the load-store
 // units to x, y and out; with mma.sync fragments straight from global
-// memory the M = 8192, R = 64 case (K = N = 3840) took 190 us, so it takes 47, where its bytes
+// memory the M = 8192, R = 64 case (K = N = 3840) took 190 us, so it takes 48.6, where its bytes
 // take 29 at the measured copy bandwidth: of a tile's time the list of tiles is 3 us, the shrink
 // 12, the exchange of v 5 and the expand 21, which alone is near that bandwidth.
 //
@@ -49,14 +49,18 @@ constexpr int kYStage = 2 * kOp;               // a 128 x 128 block of y: two bo
 // Offset of row r, 16-byte chunk c (0 .. 15) of a block of y.
 __device__ __forceinline__ int y_at(int r, int c) { return (c >> 3) * kOp + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 
-// RB blocks of 64 ranks.
-template <int RB>
+// Offset of a partial v's 16-byte chunk c (four ranks) of row r, in rows of `width` bytes (a multiple of 256): no two
+// lanes of eight that hold chunk c of eight rows meet in a bank.
+__device__ __forceinline__ int part_at(int r, int c, int width) { return r * width + ((c ^ (r & 7)) << 4); }
+
+// RB blocks of 64 ranks, v as P numbers.
+template <int RB, int P>
 struct LoraTc {
   static constexpr int kStageA = RB * 64 * 128;                        // A: up to 64 RB rows
   static constexpr int kStage = kOp + kStageA;
-  static constexpr int kPart = (128 * (64 * RB + 4) * 4 + 1023) / 1024 * 1024;   // partial v
-  static constexpr int kV = kPart;                                     // offset of v: [RB][hi, lo]
-  static constexpr int kB = kV + RB * 2 * kOp;                         // offset of B's ring
+  static constexpr int kPartRow = 64 * RB * 4;                         // partial v: 128 rows
+  static constexpr int kV = 128 * kPartRow;                            // offset of v: [RB][P]
+  static constexpr int kB = kV + RB * P * kOp;                         // offset of B's ring
   static constexpr int kStagesB = RB == 1 ? 2 : 1;
   static constexpr int kY = kB + kStagesB * RB * kOp;                  // offset of y's ring
   static constexpr int kStagesY = RB == 1 ? 3 : 1;
@@ -135,7 +139,8 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 template <typename T, typename TY, int RB>
 __global__ void __launch_bounds__(kTcThreads, 1)
     lora_tc_kernel(const __grid_constant__ TcMaps maps, const Params p) {
-  using C = LoraTc<RB>;
+  constexpr int P = VOperand<T>::kPlanes;
+  using C = LoraTc<RB, P>;
   using Tr = awq::Traits<T>;
   using TrY = awq::Traits<TY>;
   extern __shared__ uint8_t sm_raw[];
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, nullptr, 62, 100000000ull);
     }
   } else if (warp == kWork + 1 && lane == 0) {
-    const uint32_t id = idesc_f16(128, npad, sizeof(T) == 2 && !Half2Of<T>::kScaled);
+    const uint32_t id = idesc_f16(128, npad, !VOperand<T>::kScaled);
     for (int kb = k0; kb < k1; ++kb) {
       const int i = kb - k0, s = i % C::kStages;
       if (!mbar_wait(&full[s], (i / C::kStages) & 1, abort, 63)) break;
@@ -333,7 +338,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
   if (warp < kWork) {
     tc_fence_after();
-    float* part = reinterpret_cast<float*>(area) + (32 * q + lane) * (p.R + 4);
     for (int c0 = 16 * cq; c0 < p.R; c0 += 64) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * q) << 16) + c0, v);
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
         if (c0 + i < p.R)
-          *reinterpret_cast<float4*>(part + c0 + i) =
+          *reinterpret_cast<float4*>(area + part_at(32 * q + lane, (c0 + i) >> 2, C::kPartRow)) =
               any_k ? make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
                                   __uint_as_float(v[i + 3]))
                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -379,13 +383,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool mine = i < rows && r < kTcTokens;
       float v[8] = {};
       if (mine && 8 * l < p.R) {
-        const uint32_t at = smem_u32(area) + (r * (p.R + 4) + 8 * l) * 4;
+        const uint32_t at0 = smem_u32(area) + part_at(r, 2 * l, C::kPartRow);
+        const uint32_t at1 = smem_u32(area) + part_at(r, 2 * l + 1, C::kPartRow);
         float4 a[8], b[8];                                              // all ranks' loads before the first use
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < ranks) {
-            a[k] = ld_cluster_f32x4(mapa_shared(at, k));
-            b[k] = ld_cluster_f32x4(mapa_shared(at, k) + 16);
+            a[k] = ld_cluster_f32x4(mapa_shared(at0, k));
+            b[k] = ld_cluster_f32x4(mapa_shared(at1, k));
           }
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
       }
       int ex = 0;
-      if constexpr (Half2Of<T>::kScaled) {
+      if constexpr (VOperand<T>::kScaled) {
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
@@ -405,15 +410,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ex = scale_exponent(top);
       }
       const float up = exp2_int(ex);
-      T h[8], lo[8];
+      alignas(16) T planes[P][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) split(v[j] * up, h[j], lo[j]);
+      for (int j = 0; j < 8; ++j) {
+        T part[P];
+        split(v[j] * up, part);
+#pragma unroll
+        for (int k = 0; k < P; ++k) planes[k][j] = part[k];
+      }
       if (mine && l < 2 * steps) {
-        const uint32_t at = smem_u32(area) + C::kV + (l >> 3) * 2 * kOp + r * 128 + (((l & 7) ^ (r & 7)) << 4);
+        const uint32_t at = smem_u32(area) + C::kV + (l >> 3) * P * kOp + r * 128 + (((l & 7) ^ (r & 7)) << 4);
         for (int k = d0; k < d1; ++k) {
           const uint32_t to = mapa_shared(at, k);
-          st_cluster_b32x4(to, *reinterpret_cast<const uint4*>(h));
-          st_cluster_b32x4(to + kOp, *reinterpret_cast<const uint4*>(lo));
+#pragma unroll
+          for (int i = 0; i < P; ++i) st_cluster_b32x4(to + i * kOp, *reinterpret_cast<const uint4*>(planes[i]));
         }
       }
       if (mine && l == 0)
@@ -537,17 +547,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mbar_wait(&bfull[i % C::kStagesB], (i / C::kStagesB) & 1, nullptr, 67, 100000000ull);
     }
   } else if (lane == 0) {                                               // warp 17
-    const uint32_t id = idesc_f16(128, 128, sizeof(T) == 2 && !Half2Of<T>::kScaled);
+    const uint32_t id = idesc_f16(128, 128, !VOperand<T>::kScaled);
     for (int i = 0; i < nb; ++i) {
       const int s = i % C::kStagesB;
       if (!mbar_wait(&bfull[s], (i / C::kStagesB) & 1, abort, 68)) break;
       if (!mbar_wait(&dempty[i & 1], ((i >> 1) & 1) ^ 1, abort, 69)) break;
       tc_fence_after();
-      for (int k = 0; k < 2 * steps; ++k) {                             // hi, then lo
-        const int st = k < steps ? k : k - steps, rb = st >> 2;
-        mma_f16(tmem + 128 * (i & 1), desc_kmajor_sw128(area + C::kV + (2 * rb + (k < steps ? 0 : 1)) * kOp, 32 * (st & 3)),
-                desc_kmajor_sw128(area + C::kB + (s * RB + rb) * kOp, 32 * (st & 3)), id, k > 0);
-      }
+      for (int k = 0; k < P; ++k)
+        for (int st = 0; st < steps; ++st)
+          mma_f16(tmem + 128 * (i & 1), desc_kmajor_sw128(area + C::kV + (P * (st >> 2) + k) * kOp, 32 * (st & 3)),
+                  desc_kmajor_sw128(area + C::kB + (s * RB + (st >> 2)) * kOp, 32 * (st & 3)), id, k > 0 || st > 0);
       mma_commit(&bempty[s]);
       mma_commit(&dfull[i & 1]);
     }

@@ -1,5 +1,5 @@
-"""The expert layer beside entries that dwarf the rest: what a weight of zero removes
-must not cost the other entries any of their bits.
+"""The expert layer and the adapters beside entries that dwarf the rest: what a weight of zero removes
+must not cost the other entries any of their bits. The adapters with v = x A^T whose last bits show.
 
 Tolerances. Where all values are integers whose sums stay below 2^24, every 32-bit operation is
 exact and the output is the exact value rounded once: the tests ask for equality. The others bound each
@@ -170,3 +170,45 @@ def test_moe_each_element(on_gpu, T, K, I, G, dtype, spread):
     bound = slack + u * (np.abs(ref) + slack) + torch.finfo(dtype).tiny
     assert np.isfinite(out).all()
     assert (np.abs(out - ref) <= bound).all(), f"{(np.abs(out - ref) / bound).max():.3g} of the bound"
+
+
+# ---------------------------------------------------------------- the adapters
+
+LORA = [(1, 3), (40, 3), (600, 3), (1500, 2), (300, 1100)]    # few tokens, tiles of 16 and of 128, listed tiles
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,L", LORA)
+@pytest.mark.parametrize("R", [8, 64, 72, 128])
+def test_lora_integers_come_through_exactly(on_gpu, M, L, R, dtype):
+    # v of up to 20 bits, whose last bits show in the sums
+    K, N = 64, 136
+    g = torch.Generator().manual_seed(M + R)
+    x = torch.randint(-127, 128, (M, K), generator=g).to(dtype)
+    y = torch.randint(-127, 128, (M, N), generator=g).to(dtype)
+    a = torch.randint(-127, 128, (L, R, K), generator=g).to(dtype)
+    b = torch.randint(-1, 2, (L, N, R), generator=g).to(dtype)
+    ids = torch.randint(0, L, (M,), generator=g, dtype=torch.int32).sort().values
+    scales = torch.full((L,), 2.0 ** -8)
+    ref = O.lora_add(f64(y), f64(x), f64(a), f64(b), ids.numpy(), f64(scales))
+    assert np.abs(ref).max() < 2 ** 15                      # and so below 2^23 in steps of 2^-8
+    out = on_gpu.lora_add(*[t.to(DEV) for t in (y, x, a, b, ids, scales)])
+    assert torch.equal(out.cpu(), torch.from_numpy(ref).to(dtype))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,L", LORA)
+@pytest.mark.parametrize("R", [8, 72])
+def test_lora_ranks_that_cancel(on_gpu, M, L, R, dtype):
+    # v = (1 + 2^-10 + 2^-20, -1 - 2^-10, 0 ...): what is left of their sum is 2^-20
+    K, N = 40, 72
+    x, y = torch.zeros((M, K), dtype=dtype), torch.zeros((M, N), dtype=dtype)
+    a, b = torch.zeros((L, R, K), dtype=dtype), torch.ones((L, N, R), dtype=dtype)
+    x[:, :3] = 1.0
+    a[:, 0, :3] = torch.tensor([1.0, 2.0 ** -10, 2.0 ** -20])
+    a[:, 1, :3] = torch.tensor([-1.0, -(2.0 ** -10), 0.0])
+    ids = torch.arange(M, dtype=torch.int32) * L // M
+    out = on_gpu.lora_add(*[t.to(DEV) for t in (y, x, a, b, ids)])
+    assert (out == 2.0 ** -20).all()
