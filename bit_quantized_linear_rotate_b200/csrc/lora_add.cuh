@@ -485,13 +485,13 @@ __global__ void __launch_bounds__(kThreads, RC == 1 ? 3 : 2) lora_kernel(const P
   }
   cluster_sync();
 
-  // ---- v as the expand's operand
+  // ---- v as the expand's operand; zeros past the rank (where an infinity in x has made NaN of A's zeros)
   const float as = p.scales != nullptr ? __ldg(p.scales + adapter) : 1.0f;
   for (int m = warp; m < n; m += kWarps) {
     float v[RC];
     int ex = 0;
 #pragma unroll
-    for (int i = 0; i < RC; ++i) v[i] = S.v[m][32 * i + lane];
+    for (int i = 0; i < RC; ++i) v[i] = 32 * i + lane < p.R ? S.v[m][32 * i + lane] : 0.0f;
     if constexpr (VOperand<T>::kScaled) {
       uint32_t top = 0;
 #pragma unroll

@@ -212,3 +212,24 @@ def test_lora_ranks_that_cancel(on_gpu, M, L, R, dtype):
     ids = torch.arange(M, dtype=torch.int32) * L // M
     out = on_gpu.lora_add(*[t.to(DEV) for t in (y, x, a, b, ids)])
     assert (out == 2.0 ** -20).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,L", LORA)
+@pytest.mark.parametrize("R", [8, 40, 72, 128])
+def test_lora_infinity_that_the_formula_keeps(on_gpu, M, L, R, dtype):
+    # x with an infinity, all weights positive: v and the output are that infinity, whatever the rank
+    K, N = 72, 40
+    x, y = torch.ones((M, K), dtype=dtype), torch.ones((M, N), dtype=dtype)
+    a, b = torch.full((L, R, K), 0.5, dtype=dtype), torch.full((L, N, R), 0.25, dtype=dtype)
+    x[0, 5] = float("inf")
+    x[M // 2, 70] = -float("inf")
+    ids = torch.arange(M, dtype=torch.int32) * L // M
+    out = on_gpu.lora_add(*[t.to(DEV) for t in (y, x, a, b, ids)]).cpu()
+    ref = torch.full((M, N), 1 + R * K * 0.125, dtype=torch.float64)
+    ref[0] = float("inf")
+    ref[M // 2] = -float("inf")
+    if M == 1:
+        ref[0] = float("nan")                               # both infinities in one row
+    torch.testing.assert_close(out.double(), ref.to(dtype).double(), rtol=0, atol=0, equal_nan=True)
