@@ -233,3 +233,44 @@ def test_lora_infinity_that_the_formula_keeps(on_gpu, M, L, R, dtype):
     if M == 1:
         ref[0] = float("nan")                               # both infinities in one row
     torch.testing.assert_close(out.double(), ref.to(dtype).double(), rtol=0, atol=0, equal_nan=True)
+
+
+# ------------------------------------------------------------- several callers
+
+@gpu
+def test_every_call_of_every_thread_returns_its_result(on_gpu):
+    # a call that raises in its thread fails the test, and so does one that is missing
+    from concurrent.futures import ThreadPoolExecutor
+    E, k, K, I, R, L, rounds = 8, 2, 256, 128, 16, 3, 40
+    g = torch.Generator().manual_seed(3)
+
+    def part(rows, cols):
+        return [torch.randint(0, 256, (E, rows, cols // 2), generator=g, dtype=torch.uint8).to(DEV),
+                (torch.rand((E, cols // 64, rows), generator=g) * 0.009 + 0.001).to(BF).to(DEV),
+                (torch.randn((E, cols // 64, rows), generator=g) * 0.01).to(BF).to(DEV)]
+
+    experts = part(2 * I, K) + part(K, I)
+    a, b = ((torch.randn(s, generator=g) / 16).to(BF).to(DEV) for s in ((L, R, K), (L, K, R)))
+    inputs = []
+    for M in (1, 5, 33, 64):
+        x, y = (torch.randn((M, K), generator=g).to(BF).to(DEV) for _ in range(2))
+        ids = torch.randint(-1, L, (M,), generator=g, dtype=torch.int32).to(DEV)
+        inputs.append((x, y, ids, torch.randn((M, E), generator=g).to(DEV)))
+
+    def calls(x, y, ids, logits):
+        return (on_gpu.lora_add(y, x, a, b, ids), on_gpu.moe_awq_w4a16(x, logits, k, *experts),
+                *on_gpu.moe_route(logits, k))
+
+    refs = [calls(*v) for v in inputs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [calls(*inputs[i]) for _ in range(rounds)]
+        stream.synchronize()
+        return sum(all(torch.equal(p, q) for p, q in zip(one, refs[i])) for one in got)
+
+    with ThreadPoolExecutor(len(inputs)) as pool:
+        futures = [pool.submit(work, i) for i in range(len(inputs))]
+        assert [f.result() for f in futures] == [rounds] * len(inputs)
