@@ -138,7 +138,7 @@ cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cud
   const int offset = ring_offset(p.choice.T * p.choice.k, C::sums(p.choice.T));
   cudaError_t e = set_smem_all<Tag>(kern);
   if (e != cudaSuccess) return e;
-  // Two CTAs an SM (one where the sums leave no room). The cluster size by the time expected: rounds of
+  // C::kCtas CTAs an SM (one where the sums leave no room for two). The cluster size by the time expected: rounds of
   // clusters (33 of 8 run at once, 71 of 4), each some 0.5 us a step and 0.35 us a CTA of the cluster for
   // meeting and adding up (fitted to 1 to 110 steps: 16 tokens of 64 experts, K = 2048, are fastest in
   // clusters of 8, 47.5 against 57.8 us in clusters of 4; 32 tokens of 16 experts, K = 5120, of 3, 76
@@ -147,7 +147,7 @@ cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cud
   const int tiles = p.K / kRowsTile;
   const double units = p.choice.E * (1 - std::pow(1 - std::min(1.0, (double)p.choice.k / p.choice.E), p.choice.T));
   const double steps = std::max(1.0, units) * ((p.I + 64 * C::kSubs - 1) / (64 * C::kSubs));
-  int ctas = 2, cs = 0;
+  int ctas = C::kCtas, cs = 0;
   int stages = moe_stages(offset, C::kStage, ctas);
   if (stages == 0) stages = moe_stages(offset, C::kStage, ctas = 1);
   const int smem = 1024 + offset + stages * C::kStage;

@@ -11,8 +11,8 @@
 // bounds the layer: a tile of 16 weight rows x 64 columns (512 packed bytes) takes one of
 // an SM's four schedulers 89 clocks at the measured copy bandwidth, so a tile must cost well
 // under 89 issue slots. Measured, device time and the bytes' time at the copy bandwidth: 16 tokens, top-8
-// of 64 experts, K = 2048, I = 1024 70 us (31.0); 32 tokens, top-2 of 8, K = 3840, I = 10240
-// 221 (77.8); one token 18.0 (4.4).
+// of 64 experts, K = 2048, I = 1024 60 us (31.0); 32 tokens, top-2 of 8, K = 3840, I = 10240
+// 192 (77.8; the same loads without the products 124); one token 16.7 (4.4).
 //
 // Products. The nibbles become exact 16-bit numbers u - 8 in registers, the A operands of
 // mma.sync.m16n8k16 (16 weight rows); the tokens are the columns of B. For a sub-block of 64
@@ -153,15 +153,24 @@ __device__ __forceinline__ int tile_offset(int r, int sb, int t) {
   return r * 128 + (((2 * sb + (t >> 1)) ^ (r & 7)) << 4) + 8 * (t & 1);
 }
 
+// (w & mask) | magic in one operation. `magic` must not be known to the compiler: an instruction holds one
+// immediate, and with two constants it takes two (the logical operations of a tile bound the layer then:
+// 16 tokens of 64 experts 70 us, 60 so).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+  return r;
+}
+
 // A packed word's nibbles as u - 8, exact, in four pairs of 16-bit numbers: columns (0, 4), (1, 5), (2, 6), (3, 7).
 template <typename T>
-__device__ __forceinline__ void decode(uint32_t w, uint32_t (&p)[4]) {
+__device__ __forceinline__ void decode(uint32_t w, uint32_t magic, uint32_t (&p)[4]) {
   if constexpr (std::is_same<T, __half>::value) {
     // 0x6400 | u is 1024 + u, 0x6400 | 16 u is 1024 + 16 u: one shift a word in place of three
     const __half2 bias = __float2half2_rn(-1032.0f), part = __float2half2_rn(0.0625f), rest = __float2half2_rn(-72.0f);
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      const uint32_t v = w >> (4 * i), a = (v & 0x000F000Fu) | 0x64006400u, b = (v & 0x00F000F0u) | 0x64006400u;
+      const uint32_t v = w >> (4 * i), a = and_or(v, 0x000F000Fu, magic), b = and_or(v, 0x00F000F0u, magic);
       const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), bias);
       const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&b), part, rest);
       p[i] = *reinterpret_cast<const uint32_t*>(&x);
@@ -169,19 +178,19 @@ __device__ __forceinline__ void decode(uint32_t w, uint32_t (&p)[4]) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = awq::nib_pair<T>(w, i);
+    for (int i = 0; i < 4; ++i) p[i] = awq::Traits<T>::sub2(and_or(w >> (4 * i), 0x000F000Fu, magic), awq::Traits<T>::kBias);
   }
 }
 
 // A tile of 16 weight rows x 64 columns as the A operands of four MMAs: the lane's 16 columns of rows r and r + 1.
 template <typename T>
-__device__ __forceinline__ void load_tile(const uint8_t* row0, const uint8_t* row1, uint32_t (&a)[4][4]) {
+__device__ __forceinline__ void load_tile(const uint8_t* row0, const uint8_t* row1, uint32_t magic, uint32_t (&a)[4][4]) {
   const uint2 w0 = *reinterpret_cast<const uint2*>(row0), w1 = *reinterpret_cast<const uint2*>(row1);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t p[4], q[4];
-    decode<T>(i == 0 ? w0.x : w0.y, p);
-    decode<T>(i == 0 ? w1.x : w1.y, q);
+    decode<T>(i == 0 ? w0.x : w0.y, magic, p);
+    decode<T>(i == 0 ? w1.x : w1.y, magic, q);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       a[2 * i + j][0] = p[2 * j], a[2 * i + j][1] = q[2 * j];
@@ -386,6 +395,7 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
   const int tile = tile_offset(16 * rq + 2 * g, kw, t);
   const int sc0 = (kw >> p.gsh) * 128 + 32 * rq + 4 * g, sc1 = ((kw + KW) >> p.gsh) * 128 + 32 * rq + 4 * g;
   Cursor at;
+  const uint32_t magic = awq::Traits<T>::kMagic | (uint32_t)(p.gsh >> 8);   // (gsh < 8)
   constexpr int N8 = (NT + 1) / 2;       // tiles of eight tokens
   float2 tot[2][N8][2];                  // gate and up: rows r and r + 1 for tokens 2 t and 2 t + 1 of a tile
   // One item's products with N tiles; sums in tot.
@@ -434,7 +444,7 @@ __device__ __forceinline__ void gate_up(const Maps& maps, const Params& p, int s
 #pragma unroll
         for (int m = 0; m < 2; ++m) {    // gate, up
           uint32_t a[4][4];
-          load_tile<T>(row0 + m * C::kW, row1 + m * C::kW, a);
+          load_tile<T>(row0 + m * C::kW, row1 + m * C::kW, magic, a);
           const float2 s = load_pair<T>(sp + 2 * m * C::kS), z = load_pair<T>(sp + 2 * m * C::kS + C::kS);
 #pragma unroll
           for (int tt = 0; tt < N; ++tt) {
@@ -527,6 +537,9 @@ __global__ void __maxnreg__(64)
 // the first stages are fetched before the dependency wait, the rows of h after it.
 template <int NT>
 struct Down {
+  // CTAs on an SM. With rows of h for 16 tokens a second one finds no room; the registers that it would
+  // need keep more products in flight instead (64 tokens, top-2 of 8, K = I = 4096: 154 us with half of them, 142 so).
+  static constexpr int kCtas = NT == 4 ? 1 : 2;
   static constexpr int SUB = 2;                  // sub-blocks a warp and step (1: 20 us slower at 32 tokens, 8 wide experts)
   static constexpr int kCons = 8, kThreads = 32 * (kCons + 1);
   static constexpr int kSubs = 4 * SUB;
@@ -539,7 +552,7 @@ struct Down {
 };
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(Down<NT>::kThreads, 2)
+__global__ void __launch_bounds__(Down<NT>::kThreads, Down<NT>::kCtas)
     down_kernel(const __grid_constant__ Maps maps, const Params p, int stages) {
   using C = Down<NT>;
   constexpr int SUB = C::SUB;
@@ -643,6 +656,7 @@ __global__ void __launch_bounds__(Down<NT>::kThreads, 2)
     grid_dep_wait();
     grid_dep_launch();
     const int kw = warp >> 1, rh = warp & 1;
+    const uint32_t magic = awq::Traits<__half>::kMagic | (uint32_t)(p.gsh >> 8);   // (gsh < 8)
     float* acc = sums + kw * cells + 32 * rh + 2 * g;
     const int tile = tile_offset(32 * rh + 2 * g, kw, t);
     const int sc0 = (kw >> p.gsh) * 128 + 64 * rh + 4 * g, sc1 = ((kw + 4) >> p.gsh) * 128 + 64 * rh + 4 * g;
@@ -675,7 +689,7 @@ __global__ void __launch_bounds__(Down<NT>::kThreads, 2)
           float2 sc[2], z[2];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            load_tile<__half>(row0 + m * 16 * 128, row1 + m * 16 * 128, a[m]);
+            load_tile<__half>(row0 + m * 16 * 128, row1 + m * 16 * 128, magic, a[m]);
             sc[m] = load_pair<T>(sp + 32 * m), z[m] = load_pair<T>(sp + 32 * m + C::kS);
           }
 #pragma unroll
