@@ -141,9 +141,9 @@ cudaError_t launch_down(const ck::moe::Maps& maps, const ck::moe::Params& p, cud
   // C::kCtas CTAs an SM (one where the sums leave no room for two). The cluster size by the time expected: rounds of
   // clusters (33 of 8 run at once, 71 of 4), each some 0.5 us a step and 0.35 us a CTA of the cluster for
   // meeting and adding up (fitted to 1 to 110 steps: 16 tokens of 64 experts, K = 2048, are fastest in
-  // clusters of 8, 47.5 against 57.8 us in clusters of 4; 32 tokens of 16 experts, K = 5120, of 3, 76
-  // against 87 in clusters of 2). Behind gate_up_few_kernel, beside which there is room for one CTA an
-  // SM, every CTA costs (K = 3840, one token: 17.4 us in clusters of 2, 19.3 of 4).
+  // clusters of 8, 59 against 72 us in clusters of 4; 32 tokens of 16 experts, K = 5120, of 3, 101
+  // against 119 in clusters of 2). Behind gate_up_few_kernel, beside which there is room for one CTA an
+  // SM, every CTA costs (K = I = 3840, one token: 22.3 us in clusters of 2, 27.2 of 8).
   const int tiles = p.K / kRowsTile;
   const double units = p.choice.E * (1 - std::pow(1 - std::min(1.0, (double)p.choice.k / p.choice.E), p.choice.T));
   const double steps = std::max(1.0, units) * ((p.I + 64 * C::kSubs - 1) / (64 * C::kSubs));
@@ -182,9 +182,9 @@ struct MoeWorkspace {
 
 // Which kernels a call runs. One or two tokens whose items (64 columns of h of an expert) each get
 // an SM of their own: 16 consumer warps, one CTA an SM, which routes and orders x itself (K = 2048,
-// top-8 of 64, I = 1024: 14.2 us for one token, 16.0 with prepare_kernel). With a second
-// round of items it loses: the same at two tokens 23.6 against 22.1 us, and K = 4096, I = 4096,
-// top-4 at one 31.8 against 28.4; three and four tokens lose up to 9 us and win 1 at K = 1024.
+// I = 1024: one token, top-8 of 64, 16.2 us, 17.2 with prepare_kernel; two, top-4, 16.2 and 17.8). With a second
+// round of items it gains nothing or loses: two tokens, top-8, 26.2 us either way, and K = 4096, I = 4096,
+// top-4 at one 39.9 against 37.7.
 // Else two CTAs an SM, and token tiles (of four) a unit by how many
 // tokens an expert is likely to get, the mean and three standard deviations: an expert with
 // more is read again for the rest, while room for 16 tokens in every stage costs depth of the ring.
@@ -212,7 +212,7 @@ cudaError_t launch_moe(const ck::moe::Maps& gate_up, const ck::moe::Maps& down, 
   } else {
     p.lists = ws + w.lists;
     // 1024 threads from 17 tokens on: their warps choose for one token at a time (64 tokens of 256 experts, K =
-    // 512: 52.4 us for the layer against 59.9; for fewer tokens 0.3 us slower)
+    // I = 512: 72 us for the layer against 80; for fewer tokens 0.3 us slower)
     const bool many = p.choice.T > 16;
     e = launch_pdl(many ? prepare_kernel<T, 1024> : prepare_kernel<T, 512>, dim3((unsigned)p.choice.T + 1),
                    dim3(many ? 1024 : 512), 0, st, p, 4 * tiles);
@@ -310,7 +310,7 @@ cudaError_t launch_lora_few(const ck::lora::Params& p, int64_t tiles, cudaStream
   // The cluster size by the time expected: rounds of as many clusters as run at once, each a share of a tile's
   // adapter (at 14 GB/s a CTA) and some 4 us for finding the tile and exchanging v; the number of
   // tiles, known on the device only, as that of the different ids that M draws make. (K = N = 4096, R = 16, 64
-  // adapters, 100 tokens: 11.2 us in clusters of 7, 13.0 of 4, 15.4 of 8, which need two rounds.)
+  // adapters, 100 tokens: 11.7 us, 14.1 in clusters of 4, 17.0 of 8, which need two rounds.)
   const double work = 2.0 * p.R * ((double)p.K + p.N) / 14e3;
   const double likely = std::max(1.0, (p.L + 1) * (1 - std::pow(1 - 1.0 / (p.L + 1), p.M)) + (double)p.M / kFewTile / 2);
   int cs = 1;
@@ -348,7 +348,7 @@ cudaError_t launch_lora_tc(const ck::lora::Params& p, int64_t tiles, cudaStream_
     return cudaErrorInvalidValue;
   // The cluster size by the time it is expected to take: rounds of as many clusters as run at once (15 of
   // 8 CTAs, 22 of 6), each 1 / cs of a tile's bytes (at an SM's 43 GB/s) and 6 us for the stages that
-  // wait for one another (M = 2048, K = N = 4096, R = 16, 4 adapters: 24.7 us with clusters of 6, 36.8 with
+  // wait for one another (M = 2048, K = N = 4096, R = 16, 4 adapters: 23.2 us with clusters of 6, 37.5 with
   // clusters of 8, the best if all SMs took part). The number of tiles, known on the device only, is taken
   // between that of requests of 128 tokens, each with any adapter or none, and that of all adapters in turn.
   const double work = 128.0 * (p.K + 2.0 * p.N) * 2 / 43e3, fixed = 6.0;
@@ -379,7 +379,9 @@ cudaError_t launch_lora(const ck::lora::Params& p, int tm, int64_t tiles, cudaSt
 }
 
 // Tokens of a tile, by how many tokens there are and an adapter has on average: 128 from 513 tokens on
-// (K = N = 4096, R = 16, one adapter: 512 tokens 12.3 us in tiles of 16, 16.4 of 128; 1024 tokens 23.0 and 17.1).
+// (K = N = 4096, R = 16, one adapter: 512 tokens 12.4 us in tiles of 16, 17.3 of 128; 1024 tokens 22.9 and 18.2).
+// With more adapters in memory than tokens / 32 small tiles win even where all tokens name one of them, whose weights
+// then come from L2 for each tile (2000 tokens, 64 adapters: 21.8 us, 32.3 in tiles of 128).
 int lora_tile(int64_t M, int64_t L) {
   return M > 512 && M >= 32 * L ? ck::lora::kTcTokens : ck::lora::kFewTile;
 }

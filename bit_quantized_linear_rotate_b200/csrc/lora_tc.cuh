@@ -101,12 +101,6 @@ __device__ __forceinline__ void st_cluster_b32x4(uint32_t addr, uint4 v) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 // a: (L R, K), b: (L N, R), x: (M, K), y and out: (M, N); the last two only where p.vec.
 struct TcMaps {
   CUtensorMap a, b, x, y, out;

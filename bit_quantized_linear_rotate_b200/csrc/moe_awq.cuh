@@ -296,7 +296,7 @@ constexpr int kSelfBytes = 32 * 1024;
 template <int NT, int KW, bool SELF>
 struct GateUp {
   static constexpr int kCons = 4 * KW, kThreads = 32 * (kCons + 1);
-  static constexpr int kCtas = KW == 4 ? 1 : 2;     // on an SM (three with shallower rings: 49 against 46.5 us at 16 tokens)
+  static constexpr int kCtas = KW == 4 ? 1 : 2;     // on an SM (three with shallower rings: 63.5 against 60.2 us at 16 tokens)
   static constexpr int kSubs = 2 * KW;                          // sub-blocks a stage
   static constexpr int kW = kSubs * 64 * 32;                    // its bytes of gate (or up) weights
   static constexpr int kS = kSubs * 128;                        // bytes of each kind of scales
@@ -540,7 +540,7 @@ struct Down {
   // CTAs on an SM. With rows of h for 16 tokens a second one finds no room; the registers that it would
   // need keep more products in flight instead (64 tokens, top-2 of 8, K = I = 4096: 154 us with half of them, 142 so).
   static constexpr int kCtas = NT == 4 ? 1 : 2;
-  static constexpr int SUB = 2;                  // sub-blocks a warp and step (1: 20 us slower at 32 tokens, 8 wide experts)
+  static constexpr int SUB = 2;                  // sub-blocks a warp and step (1: 64.3 against 60.2 us at 16 tokens of 64 experts)
   static constexpr int kCons = 8, kThreads = 32 * (kCons + 1);
   static constexpr int kSubs = 4 * SUB;
   static constexpr int kW = kSubs * 64 * 32;
