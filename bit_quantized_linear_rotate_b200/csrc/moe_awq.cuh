@@ -45,7 +45,7 @@
 namespace ck {
 namespace moe {
 
-constexpr int kColsItem = 64;          // columns of h in one item of gate_up_kernel: one block of the fixed point
+constexpr int kColsItem = 64;          // columns of h in one item of gate_up_kernel: one sub-block of down_kernel
 constexpr int kRowsTile = 64;          // output columns of one cluster of down_kernel
 constexpr int kMaxStages = 6;
 
@@ -287,7 +287,7 @@ __device__ __forceinline__ uint8_t* align_1024(uint8_t* p) { return p + ((1024 -
 // ran for 45 us and others for 128), and streams its weights, with the unit's rows of x,
 // 128 KW columns a stage. Consumer warp (kw, rq) multiplies 16 gate and 16 up rows with sub-blocks kw
 // and kw + KW of each stage; the KW partial sums meet in shared memory, where
-// one warp a token forms h and converts it to fixed point.
+// one warp a token forms h, as hi + lo.
 //
 // SELF: every CTA routes and converts x itself, into shared memory (T <= kFewTokens): the
 // launch of prepare_kernel and the wait for it cost more.
