@@ -444,7 +444,9 @@ ck_status ck_moe_experts_awq_w4a16(const void* x, ck_dtype dt, int64_t T, int64_
  * all of them share (any linear of this library):
  *   out[m] = y[m] + scales[a] * ((x[m] A[a]^T) B[a]^T),   a = ids[m]
  *   out[m] = y[m]                                         where a is outside [0, L)
- * in float32, rounded once, to yt.
+ * in float32, rounded once, to yt; x A[a]^T, a float32 sum, enters the second
+ * product with all its bits (xt bf16) or to 2^-23 of itself or 2^-38 of its row's
+ * largest (fp16). A row of x that is not finite shows in its own output only.
  * x      : (M, K) bf16 or fp16 (xt), row stride ldx >= K, ldx % 8 == 0.
  * y, out : (M, N), bf16 or xt (yt), row strides ldy, ldo >= N elements. out may be
  *          y itself with the same stride; otherwise it must not overlap y, and
